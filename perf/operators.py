@@ -207,7 +207,7 @@ def _prepare_own(st):
 def _quantise(x):
     """fp32 [..., k]: E4M3 codes and the power-of-two scale of each row: the smallest 2^e with
     amax <= 448 * 2^e, e in [-100, 100]; 1 for a row of zeros. amax is over the finite values;
-    infinities become the largest code, NaN stays NaN."""
+    infinities become the largest code, NaN E4M3's NaN."""
     mag = x.abs()
     amax = torch.where(torch.isfinite(x), mag, torch.zeros_like(mag)).amax(dim=-1)
     m, e = torch.frexp(amax)
@@ -230,6 +230,7 @@ def _run_write(st):
     groups = -(-dl // GROUP)
     lat = torch.nn.functional.pad(x[:, :dl], (0, groups * GROUP - dl)).view(-1, groups, GROUP)
     codes, scales = _quantise(lat)
+    scales = scales.masked_fill(lat.isnan().any(dim=-1), math.nan)      # a group that holds a NaN reads as NaN
     c = st["cache"]
     c["codes"][seq, at] = codes.reshape(-1, groups * GROUP)[:, :dl]
     c["scales"][seq, at] = scales
