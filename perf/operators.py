@@ -54,13 +54,13 @@ def listed():
         {"name": "sparse tiny", "op": "sparse", "dims": "tiny", "batch": 2, "n": 100, "max_len": 501, "topk": 77},
         # a tree of 16 drafted tokens after one long context
         {"name": "tree 1x16", "op": "tree", "dims": "prod", "batch": 1, "n": 16, "max_len": 131072, "topk": 2048,
-         "cache8": True},
+         "qcache": True},
         # drafted trees of a batch, the largest that fill one 64-row block and one row more
         {"name": "tree 4x65", "op": "tree", "dims": "prod", "batch": 4, "n": 65, "max_len": 16384, "topk": 1500,
-         "cache8": True},
+         "qcache": True},
         # drafted trees over the bf16 cache
         {"name": "tree bf16 16x8", "op": "tree", "dims": "prod", "batch": 16, "n": 8, "max_len": 8192, "topk": 2048,
-         "cache8": False},
+         "qcache": False},
     ]
 
 
@@ -92,7 +92,7 @@ def draw(rng):
     n = _log_int(rng, 1, 200)
     batch = _log_int(rng, 1, max(1, 600 // n))
     return {"op": op, "dims": dims, "batch": batch, "n": n, "max_len": n + _log_int(rng, 1, 16000), "topk": topk,
-            "cache8": rng.random() < 0.6}
+            "qcache": rng.random() < 0.6}
 
 
 # ----------------------------------------------------------------------------- inputs
@@ -127,7 +127,7 @@ def _selection(g, lengths, n, topk, max_len):
     return torch.where(pos < ln, pos, torch.full_like(pos, -1.0)).to(torch.int32)
 
 
-def _cache8(g, d, batch, max_len):
+def _qcache(g, d, batch, max_len):
     codes = (torch.randn((batch, max_len, d["d_latent"]), generator=g, device="cuda") * 100.0).clamp(-448, 448)
     groups = -(-d["d_latent"] // GROUP)
     e = torch.randint(-8, -5, (batch, max_len, groups), generator=g, device="cuda")
@@ -161,15 +161,15 @@ def prepare(case, seed):
         st["k_idx"] = torch.zeros((b, max_len, d["idx_dim"]), dtype=torch.uint8, device="cuda")
         st["k_scale"] = torch.zeros((b, max_len), device="cuda")
     elif case["op"] == "read":
-        st["cache"] = _cache8(g, d, b, max_len)
+        st["cache"] = _qcache(g, d, b, max_len)
         st["lengths"] = _lengths(g, b, 1, max_len)
         st["start"] = torch.zeros((b,), dtype=torch.int32, device="cuda")
         st["rows"] = None
         if case["listed"]:
             st["rows"] = _selection(g, st["lengths"], 1, n, max_len).view(b, n)
     else:
-        if case.get("cache8", True):
-            st["cache"] = _cache8(g, d, b, max_len)
+        if case.get("qcache", True):
+            st["cache"] = _qcache(g, d, b, max_len)
         else:
             st["kv"] = _latents(g, b, max_len, width)
         lengths = _lengths(g, b, 1, max_len)
@@ -197,10 +197,10 @@ def _prepare_own(st):
     st["dsa"] = dsa
     st["dims"] = dsa.make_dims(case["batch"], case["n"], case["max_len"], idx_dim=d["idx_dim"], n_heads=d["heads"],
                                d_latent=d["d_latent"], d_rope=d["d_rope"], softmax_scale=st.get("scale"))
-    st["ws"] = dsa.Workspace.create_cache8(st["dims"], case.get("topk", 1))
+    st["ws"] = dsa.Workspace.create_qcache(st["dims"], case.get("topk", 1))
     if "cache" in st:
         c = st["cache"]
-        st["handle"] = dsa.Cache8(c["codes"], c["scales"], c["rope"], st.get("k_idx"), st.get("k_scale"))
+        st["handle"] = dsa.QCache(c["codes"], c["scales"], c["rope"], st.get("k_idx"), st.get("k_scale"))
 
 
 # ----------------------------------------------------------------------------- plain forms
@@ -330,16 +330,16 @@ def run(st):
 def _run_own(st, op):
     dsa = st["dsa"]
     if op == "write":
-        dsa.cache8_write(st["dims"], st["handle"], st["latent"], st["keys"], st["ws"], start=st["start"],
+        dsa.qcache_write(st["dims"], st["handle"], st["latent"], st["keys"], st["ws"], start=st["start"],
                          lengths=st["lengths"], src_rows=st["src"])
         return _written(st)
     if op == "read":
         if st["rows"] is not None:
-            return dsa.cache8_read(st["dims"], st["handle"], st["ws"], rows=st["rows"])
-        return dsa.cache8_read(st["dims"], st["handle"], st["ws"], start=st["start"], lengths=st["lengths"])
+            return dsa.qcache_read(st["dims"], st["handle"], st["ws"], rows=st["rows"])
+        return dsa.qcache_read(st["dims"], st["handle"], st["ws"], start=st["start"], lengths=st["lengths"])
     topk = st["case"]["topk"]
     if op == "sparse":
-        return dsa.sparse_mla_attn_cache8(st["dims"], st["q"], st["handle"], st["idx"], topk, st["ws"])
+        return dsa.sparse_mla_attn_qcache(st["dims"], st["q"], st["handle"], st["idx"], topk, st["ws"])
     return dsa.tree_mla_attn(st["dims"], st["q"], st["handle"] if "cache" in st else st["kv"], st["idx"], topk,
                              st["draft"], st["parents"], st["ws"])
 
@@ -447,7 +447,7 @@ def work(case):
         return {"bytes": b * n * (row8 * 0.75 + 2 * width), "flops": 0}
     topk, h = case["topk"], d["heads"]
     rows = min(b * n * topk, b * case["max_len"])
-    bytes_ = rows * (row8 if case.get("cache8", True) else 2 * width)
+    bytes_ = rows * (row8 if case.get("qcache", True) else 2 * width)
     bytes_ += b * n * (2 * h * width + 2 * h * d["d_latent"] + 4 * h + 4 * topk)
     pairs = b * n * topk
     if case["op"] == "tree":
