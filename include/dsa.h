@@ -194,6 +194,101 @@ dsa_status dsa_indexer_topk_decode_noalloc(const dsa_dims* dims, const void* q_i
                                            const void* k_idx, const float* scales, const int32_t* lengths,
                                            int32_t topk, int32_t* out_idx, uint32_t* status, dsa_stream_t stream);
 
+/*
+ * The 8-bit latent cache. A token's row is d_latent E4M3 codes, one scale per group of 128 of
+ * them (the last group may be shorter), and the RoPE part in bf16: 656 bytes at the production
+ * dims, against 1152 in the bf16 cache of the calls above. All three arrays are caller-owned
+ * device memory. With amax the largest finite magnitude of a group, dsa_qcache_write takes
+ *   scale = 2^e, e the smallest integer with amax <= 448 * 2^e, held to -100..100 (1 if amax is 0)
+ *   code  = E4M3(x / scale), round to nearest even
+ * Infinities, and magnitudes above 448 * 2^100, become the largest code; a group that holds a NaN
+ * gets the scale NaN and reads as NaN throughout. code * scale is exact in bf16. A cache filled by
+ * other means must hold scales of that form (powers of two, or NaN) and no NaN codes (0x7F, 0xFF).
+ * The calls on an 8-bit cache require d_latent % 16 == 0 (else DSA_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  void* codes;    /* E4M3 [B, max_len, d_latent]                  (16-byte aligned) */
+  float* scales;  /* fp32 [B, max_len, ceil(d_latent / 128)]                        */
+  void* rope;     /* bf16 [B, max_len, d_rope]  (16-byte aligned; NULL if d_rope is 0) */
+} dsa_qcache;
+
+/* Bytes of workspace that dsa_sparse_mla_attn_qcache, dsa_tree_mla_attn and
+ * dsa_tree_mla_attn_qcache need for these dims and top-k (256-byte aligned pointer required;
+ * initialise it with dsa_workspace_init). dsa_qcache_write and dsa_qcache_read use the status word
+ * only: 256 bytes of any workspace. Returns 0 for invalid dims. Pure host function. */
+size_t dsa_qcache_workspace_bytes(const dsa_dims* dims, int32_t topk);
+
+/*
+ * Quantises n_q new rows per sequence into an 8-bit cache, and their index keys into the FP8 form
+ * that dsa_indexer_topk reads (one scale per token, same rule; a NaN becomes E4M3's NaN there).
+ * Row j of sequence b goes to position start[b] + j. It is written when that position is in
+ * [0, lengths[b]), so a padded batch writes its sequences' own rows and leaves every other row of
+ * the cache as it was; a position >= max_len, or a source row >= n_src, is reported as
+ * DSA_ERR_INDEX_RANGE and skipped.
+ *   latent    bf16 [B, n_src, d_latent + d_rope]  (16-byte aligned), or NULL: keys only
+ *   keys      bf16 [B, n_src, idx_dim]            (16-byte aligned), or NULL: latents only
+ *   src_rows  int32 [B, n_q], or NULL. The source row of each written row, < 0 for none: the
+ *             accepted path of a drafted tree is committed by listing its nodes. NULL: row j is
+ *             source row j (then n_src >= n_q).
+ *   start     int32 [B], or NULL: 0
+ *   lengths   int32 [B], or NULL: max_len. The sequences' lengths after the call.
+ *   cache     the rows' destination (unused, may be NULL, without latent)
+ *   k_idx     E4M3 [B, max_len, idx_dim] (16-byte aligned), k_scale fp32 [B, max_len]: the keys'
+ *             destination (unused, may be NULL, without keys)
+ */
+dsa_status dsa_qcache_write(const dsa_dims* dims, const void* latent, const void* keys, int32_t n_src,
+                            const int32_t* src_rows, const int32_t* start, const int32_t* lengths,
+                            const dsa_qcache* cache, void* k_idx, float* k_scale, void* ws, size_t ws_bytes,
+                            dsa_stream_t stream);
+
+/*
+ * Reads rows of an 8-bit cache back as bf16 (exact: the values the attention over the cache uses),
+ * for the calls that take a bf16 cache.
+ *   rows_listed  int32 [B, n_q] positions, < 0: a row of zeros; >= max_len is reported as
+ *                DSA_ERR_INDEX_RANGE and gives a row of zeros. start and lengths are then unused.
+ *                NULL: row j of sequence b is position start[b] + j where that is in
+ *                [0, min(lengths[b], max_len)), a row of zeros elsewhere
+ *   start        int32 [B], or NULL: 0
+ *   lengths      int32 [B], or NULL: max_len
+ *   out          bf16 [B, n_q, d_latent + d_rope]  (16-byte aligned)
+ */
+dsa_status dsa_qcache_read(const dsa_dims* dims, const dsa_qcache* cache, const int32_t* rows_listed,
+                           const int32_t* start, const int32_t* lengths, void* out, void* ws, size_t ws_bytes,
+                           dsa_stream_t stream);
+
+/*
+ * dsa_sparse_mla_attn over an 8-bit cache: the same arguments, layouts and result (index rules and
+ * duplicates included), with the rows' values as dsa_qcache_read gives them. A query's rows are
+ * split over several CTAs when there are few queries (decode). softmax_scale must be positive.
+ * Workspace: dsa_qcache_workspace_bytes.
+ */
+dsa_status dsa_sparse_mla_attn_qcache(const dsa_dims* dims, const void* q, const dsa_qcache* cache,
+                                      const int32_t* idx, int32_t topk, void* out, float* lse, void* ws,
+                                      size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens behind a cache, to verify several continuations of each
+ * sequence in one step. Query i of sequence b is node i of its tree; its attended rows are the
+ * cache rows idx[b,i,:] lists (index rules of dsa_sparse_mla_attn; a list of -1 for an empty
+ * context) and the drafted rows on its path: itself, its parent, and so on. The drafted rows are
+ * not in the cache; dsa_qcache_write commits the accepted ones.
+ *   draft    bf16  [B, n_q, d_latent + d_rope]  (16-byte aligned) latent row of each node
+ *   parents  int32 [B, n_q]  the node's parent: an earlier node (0 <= parents[b,i] < i), -1 for a
+ *            child of the last committed token, < -1 for an absent node (padding). An absent node,
+ *            and a node below one, gives out = 0 and lse = -inf; a parent >= i is reported as
+ *            DSA_ERR_INDEX_RANGE and the node, and those below it, count as absent.
+ * Rows off a node's path have no effect on it, whatever they hold. The selection of a node over the
+ * committed tokens is dsa_indexer_topk's with n_q = 1 and that node's index query.
+ * n_q <= 256 (else DSA_ERR_UNSUPPORTED); softmax_scale must be positive.
+ * Workspace: dsa_qcache_workspace_bytes, for both forms.
+ */
+dsa_status dsa_tree_mla_attn(const dsa_dims* dims, const void* q, const void* latent_kv, const int32_t* idx,
+                             int32_t topk, const void* draft, const int32_t* parents, void* out, float* lse, void* ws,
+                             size_t ws_bytes, dsa_stream_t stream);
+dsa_status dsa_tree_mla_attn_qcache(const dsa_dims* dims, const void* q, const dsa_qcache* cache, const int32_t* idx,
+                                    int32_t topk, const void* draft, const int32_t* parents, void* out, float* lse,
+                                    void* ws, size_t ws_bytes, dsa_stream_t stream);
+
 /* Synchronises `stream`, returns the first device-side error recorded in `ws` since the
  * last call (DSA_OK if none) and clears it. `detail`, if non-NULL, receives a location tag. */
 dsa_status dsa_get_device_status(void* ws, dsa_stream_t stream, uint32_t* detail);

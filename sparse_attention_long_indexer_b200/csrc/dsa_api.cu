@@ -17,6 +17,8 @@
 #include "decode_select.cuh"
 #include "sparse_mla.cuh"
 #include "indexer_kl.cuh"
+#include "qcache.cuh"
+#include "cache_attn.cuh"
 
 namespace dsa {
 
@@ -214,6 +216,12 @@ DeviceInfo device_info() {
     cudaFuncSetAttribute(sparse_mla_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          AttnCfg::SMEM_BYTES);
     cudaFuncSetAttribute(indexer_kl_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, KlCfg::SMEM_BYTES);
+    cudaFuncSetAttribute(cache_attn_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         CacheAttnCfg::SMEM_BYTES);
+    cudaFuncSetAttribute(cache_attn_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         CacheAttnCfg::SMEM_BYTES);
+    cudaFuncSetAttribute(cache_attn_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         CacheAttnCfg::SMEM_BYTES);
     cudaFuncAttributes fa{};
     cache[dev].indexer_regs_ok = cudaFuncGetAttributes(&fa, indexer_topk_kernel<kPrefillNQ>) == cudaSuccess &&
                                  fa.numRegs == IdxCfg<kPrefillNQ>::LAUNCH_REGS;
@@ -259,6 +267,20 @@ bool encode_q_bf16(CUtensorMap* map, const void* base, uint64_t rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDqk), rows, 1};
   const cuuint64_t strides[2] = {kDqk * 2, rows * kDqk * 2};
   const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Queries of any supported dims as a 2-D bf16 tensor [rows = B*n_q*n_heads, d], box {64 dims, 128 rows}.
+// Rows and dims past the tensor's end are filled with zeros.
+bool encode_q_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t d) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {d, rows, 1};
+  const cuuint64_t strides[2] = {d * 2, rows * d * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kHeads), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -775,3 +797,259 @@ extern "C" dsa_status dsa_indexer_topk_decode_noalloc(const dsa_dims* dims, cons
   merge_partials_kernel<kMergeThreads><<<d.batch, kMergeThreads, 0, st>>>(mp);
   return from_cuda(cudaGetLastError());
 }
+
+// ----------------------------------------------------------------------------- 8-bit cache, drafted trees
+namespace {
+
+// dims of the calls on an 8-bit cache: whole 16-byte chunks of codes
+dsa_status check_dims8(const dsa_dims* dims, int32_t topk) {
+  const dsa_status s = check_dims(dims, topk);
+  if (s != DSA_OK) return s;
+  return dims->d_latent % 16 == 0 ? DSA_OK : DSA_ERR_UNSUPPORTED;
+}
+
+dsa_status check_qcache(const dsa_dims& d, const dsa_qcache* c) {
+  if (c == nullptr || c->codes == nullptr || c->scales == nullptr || (d.d_rope > 0 && c->rope == nullptr))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(c->codes, 16) || !aligned(c->scales, 4) || !aligned(c->rope, 16)) return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+QCacheView view(const dsa_qcache& c) {
+  return QCacheView{static_cast<uint8_t*>(c.codes), c.scales, static_cast<__nv_bfloat16*>(c.rope)};
+}
+
+// status word only: all that the row kernels use of a workspace
+dsa_status check_status_ws(void* ws, size_t ws_bytes) {
+  return ws == nullptr || !aligned(ws, kAlign) || ws_bytes < kAlign ? DSA_ERR_WORKSPACE : DSA_OK;
+}
+
+// One warp per row, as many CTAs as there are rows for up to 8 resident ones per SM.
+int row_grid(int64_t rows, int sms) {
+  return static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, static_cast<int64_t>(8) * sms));
+}
+
+// How the rows of a query are split (see cache_attn.cuh). The cost of a split is what the slowest
+// SM does: its items one after another, each a fixed part (q, statistics, output) and its blocks,
+// and, with more than one range, the join: a launch, and the ranges' outputs written and read.
+struct CachePlan {
+  int32_t n_halves, n_splits, split_blocks;
+};
+constexpr int64_t kPlanSms = 148;
+constexpr int64_t kPlanItemNs = 2500, kPlanBlockNs = 1200, kPlanJoinNs = 3000, kPlanPartNs = 130;
+CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
+  CachePlan best{d.d_latent > CacheAttnCfg::OUT_DIMS ? 2 : 1, 1, 1};
+  const int64_t queries = static_cast<int64_t>(d.batch) * d.n_q;
+  const int32_t blocks = (topk + CacheAttnCfg::BLK - 1) / CacheAttnCfg::BLK +
+                         (tree ? (d.n_q + CacheAttnCfg::BLK - 1) / CacheAttnCfg::BLK : 0);
+  best.split_blocks = blocks;
+  int64_t least = -1;
+  for (int32_t per = blocks; per >= 1; --per) {
+    const int32_t splits = (blocks + per - 1) / per;
+    if (least >= 0 && splits == best.n_splits) continue;
+    const int64_t items = queries * splits * best.n_halves;
+    const int64_t waves = (items + kPlanSms - 1) / kPlanSms;
+    int64_t cost = waves * (kPlanItemNs + per * kPlanBlockNs);
+    if (splits > 1) cost += kPlanJoinNs + kPlanPartNs * queries * splits;
+    if (least < 0 || cost < least) {
+      least = cost;
+      best.n_splits = splits;
+      best.split_blocks = (blocks + splits - 1) / splits;
+    }
+  }
+  return best;
+}
+
+// Workspace of the attention calls on caches: status word, then the ranges' outputs and statistics.
+struct CacheLayout {
+  size_t part_out = 0, part_lse = 0, total = 0;
+};
+CacheLayout cache_layout(const dsa_dims& d, const CachePlan& plan) {
+  CacheLayout L;
+  size_t off = kAlign;
+  if (plan.n_splits > 1) {
+    const size_t rows = static_cast<size_t>(d.batch) * d.n_q * plan.n_splits * d.n_heads;
+    L.part_out = off; off = align_up(off + rows * d.d_latent * 4);
+    L.part_lse = off; off = align_up(off + rows * 4);
+  }
+  L.total = off;
+  return L;
+}
+
+template <bool kQuant, bool kTree>
+dsa_status launch_cache_attn(const CUtensorMap& map_q, const CacheAttnParams& p, int sms, cudaStream_t st) {
+  const int grid = static_cast<int>(std::min<int64_t>(p.n_items, sms));
+  cache_attn_kernel<kQuant, kTree><<<grid, CacheAttnCfg::THREADS, CacheAttnCfg::SMEM_BYTES, st>>>(map_q, p);
+  return from_cuda(cudaGetLastError());
+}
+
+// The attention over an 8-bit cache (cache != null) or a bf16 one (kv), with a drafted tree or without.
+dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache* cache, const void* kv,
+                           const int32_t* idx, int32_t topk, bool tree, const void* draft, const int32_t* parents,
+                           void* out, float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  dsa_status s = cache != nullptr ? check_dims8(dims, topk) : check_dims(dims, topk);
+  if (s != DSA_OK) return s;
+  const dsa_dims& d = *dims;
+  if (!(d.softmax_scale > 0.f)) return DSA_ERR_INVALID_ARG;
+  if (tree && d.n_q > kMaxDraft) return DSA_ERR_UNSUPPORTED;
+  const int64_t queries = static_cast<int64_t>(d.batch) * d.n_q;
+  const CachePlan plan = plan_cache(d, topk, tree);
+  const CacheLayout L = cache_layout(d, plan);
+  if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
+  if (queries == 0) return DSA_OK;
+  if (queries * d.n_heads >= (int64_t(1) << 31) || queries * plan.n_splits * plan.n_halves >= (int64_t(1) << 31))
+    return DSA_ERR_UNSUPPORTED;
+  if (!q || !idx || !out || !lse || (cache == nullptr && !kv) || (tree && (!draft || !parents)))
+    return DSA_ERR_INVALID_ARG;
+  if (cache != nullptr && (s = check_qcache(d, cache)) != DSA_OK) return s;
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(idx, 4) || !aligned(draft, 16) || !aligned(parents, 4) ||
+      !aligned(out, 16) || !aligned(lse, 4))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = device_ok()) != DSA_OK) return s;
+  const DeviceInfo dev = device_info();
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  CacheAttnParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  if (cache != nullptr) p.cache = view(*cache);
+  p.idx = idx;
+  p.draft = static_cast<const __nv_bfloat16*>(draft);
+  p.parents = parents;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.part_out = reinterpret_cast<float*>(wsb + L.part_out);
+  p.part_lse = reinterpret_cast<float*>(wsb + L.part_lse);
+  p.status = reinterpret_cast<uint32_t*>(wsb);
+  p.n_q = d.n_q;
+  p.max_len = d.max_len;
+  p.topk = topk;
+  p.n_heads = d.n_heads;
+  p.d_latent = d.d_latent;
+  p.d_rope = d.d_rope;
+  p.n_halves = plan.n_halves;
+  p.n_splits = plan.n_splits;
+  p.split_blocks = plan.split_blocks;
+  p.n_items = static_cast<int32_t>(queries * plan.n_splits * plan.n_halves);
+  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  p.wait_budget_ns = kWaitBudgetNs;
+  CUtensorMap map_q;
+  if (!encode_q_rows(&map_q, q, static_cast<uint64_t>(queries) * d.n_heads,
+                     static_cast<uint64_t>(d.d_latent + d.d_rope)))
+    return DSA_ERR_CUDA;
+  if (cache == nullptr) s = launch_cache_attn<false, true>(map_q, p, dev.sms, st);
+  else if (tree) s = launch_cache_attn<true, true>(map_q, p, dev.sms, st);
+  else s = launch_cache_attn<true, false>(map_q, p, dev.sms, st);
+  if (s != DSA_OK || plan.n_splits == 1) return s;
+  cache_attn_join_kernel<<<static_cast<unsigned>(queries * d.n_heads), kJoinThreads, 0, st>>>(
+      p.part_out, p.part_lse, p.out, p.lse, plan.n_splits, d.n_heads, d.d_latent);
+  return from_cuda(cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_qcache_workspace_bytes(const dsa_dims* dims, int32_t topk) {
+  if (check_dims(dims, topk) != DSA_OK) return 0;
+  const size_t listed = cache_layout(*dims, plan_cache(*dims, topk, false)).total;
+  if (dims->n_q > kMaxDraft) return listed;
+  return std::max(listed, cache_layout(*dims, plan_cache(*dims, topk, true)).total);
+}
+
+dsa_status dsa_qcache_write(const dsa_dims* dims, const void* latent, const void* keys, int32_t n_src,
+                            const int32_t* src_rows, const int32_t* start, const int32_t* lengths,
+                            const dsa_qcache* cache, void* k_idx, float* k_scale, void* ws, size_t ws_bytes,
+                            dsa_stream_t stream) {
+  NvtxRange range("qcache_write");
+  dsa_status s = check_dims8(dims, 1);
+  if (s != DSA_OK) return s;
+  const dsa_dims& d = *dims;
+  if (n_src < 0 || (src_rows == nullptr && n_src < d.n_q)) return DSA_ERR_INVALID_ARG;
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  const int64_t rows = static_cast<int64_t>(d.batch) * d.n_q;
+  if (rows == 0) return DSA_OK;
+  if (latent == nullptr && keys == nullptr) return DSA_ERR_INVALID_ARG;
+  if (latent != nullptr && (s = check_qcache(d, cache)) != DSA_OK) return s;
+  if (keys != nullptr && (!k_idx || !k_scale)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(latent, 16) || !aligned(keys, 16) || !aligned(src_rows, 4) || !aligned(start, 4) ||
+      !aligned(lengths, 4) || !aligned(k_idx, 16) || !aligned(k_scale, 4))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = device_ok()) != DSA_OK) return s;
+  QCacheWriteParams p{};
+  p.latent = static_cast<const __nv_bfloat16*>(latent);
+  p.keys = static_cast<const __nv_bfloat16*>(keys);
+  p.src = src_rows;
+  p.start = start;
+  p.lengths = lengths;
+  if (latent != nullptr) p.cache = view(*cache);
+  p.k_idx = static_cast<uint8_t*>(k_idx);
+  p.k_scale = k_scale;
+  p.status = static_cast<uint32_t*>(ws);
+  p.n = d.n_q;
+  p.n_src = n_src;
+  p.max_len = d.max_len;
+  p.d_latent = d.d_latent;
+  p.d_rope = d.d_rope;
+  p.idx_dim = d.idx_dim;
+  p.rows = rows;
+  qcache_write_kernel<<<row_grid(rows, device_info().sms), kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return from_cuda(cudaGetLastError());
+}
+
+dsa_status dsa_qcache_read(const dsa_dims* dims, const dsa_qcache* cache, const int32_t* rows_listed,
+                           const int32_t* start, const int32_t* lengths, void* out, void* ws, size_t ws_bytes,
+                           dsa_stream_t stream) {
+  NvtxRange range("qcache_read");
+  dsa_status s = check_dims8(dims, 1);
+  if (s != DSA_OK) return s;
+  const dsa_dims& d = *dims;
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  const int64_t rows = static_cast<int64_t>(d.batch) * d.n_q;
+  if (rows == 0) return DSA_OK;
+  if ((s = check_qcache(d, cache)) != DSA_OK) return s;
+  if (out == nullptr || !aligned(out, 16) || !aligned(rows_listed, 4) || !aligned(start, 4) || !aligned(lengths, 4))
+    return DSA_ERR_INVALID_ARG;
+  if ((s = device_ok()) != DSA_OK) return s;
+  QCacheReadParams p{};
+  p.cache = view(*cache);
+  p.listed = rows_listed;
+  p.start = start;
+  p.lengths = lengths;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.status = static_cast<uint32_t*>(ws);
+  p.n = d.n_q;
+  p.max_len = d.max_len;
+  p.d_latent = d.d_latent;
+  p.d_rope = d.d_rope;
+  p.rows = rows;
+  qcache_read_kernel<<<row_grid(rows, device_info().sms), kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return from_cuda(cudaGetLastError());
+}
+
+dsa_status dsa_sparse_mla_attn_qcache(const dsa_dims* dims, const void* q, const dsa_qcache* cache,
+                                      const int32_t* idx, int32_t topk, void* out, float* lse, void* ws,
+                                      size_t ws_bytes, dsa_stream_t stream) {
+  NvtxRange range("sparse_mla_attn_qcache");
+  static const dsa_qcache kNone = {nullptr, nullptr, nullptr};
+  return cache_attention(dims, q, cache != nullptr ? cache : &kNone, nullptr, idx, topk, false, nullptr, nullptr, out,
+                         lse, ws, ws_bytes, stream);
+}
+
+dsa_status dsa_tree_mla_attn(const dsa_dims* dims, const void* q, const void* latent_kv, const int32_t* idx,
+                             int32_t topk, const void* draft, const int32_t* parents, void* out, float* lse, void* ws,
+                             size_t ws_bytes, dsa_stream_t stream) {
+  NvtxRange range("tree_mla_attn");
+  return cache_attention(dims, q, nullptr, latent_kv, idx, topk, true, draft, parents, out, lse, ws, ws_bytes, stream);
+}
+
+dsa_status dsa_tree_mla_attn_qcache(const dsa_dims* dims, const void* q, const dsa_qcache* cache, const int32_t* idx,
+                                    int32_t topk, const void* draft, const int32_t* parents, void* out, float* lse,
+                                    void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  NvtxRange range("tree_mla_attn_qcache");
+  static const dsa_qcache kNone = {nullptr, nullptr, nullptr};
+  return cache_attention(dims, q, cache != nullptr ? cache : &kNone, nullptr, idx, topk, true, draft, parents, out,
+                         lse, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

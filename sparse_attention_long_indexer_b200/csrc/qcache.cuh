@@ -1,0 +1,243 @@
+// The 8-bit latent cache: rows quantised as they are written, and read back.
+//
+// A row of the cache is d_latent E4M3 codes, one fp32 scale per group of 128 of them, and the
+// RoPE part in bf16 (656 B at the production dims, against 1152 B in bf16). With amax the
+// largest finite magnitude of a group,
+//   scale = 2^e, e the smallest integer with amax <= 448 * 2^e, held to -100 .. 100 (1 if amax = 0)
+//   code  = E4M3(x / scale), to nearest even, magnitudes above 448 * scale held to 448
+// A power of two costs nothing (E4M3's spacing is relative) and makes x / scale exact, so the
+// code is the only rounding; and code * scale is exact in bf16 (E4M3 has 4 significant bits),
+// so reading back rounds nothing. A group that holds a NaN gets the scale NaN and reads as NaN.
+// Index keys are quantised by the same rule with one scale per token, the form the indexer takes.
+//
+// Both kernels move bytes and compute next to nothing: one warp per row, every lane one 16-code
+// chunk, all loads of a row issued before the first use.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+
+namespace dsa {
+
+constexpr int kScaleGroup = 128;         // latent dims per scale
+constexpr int kScaleExpMax = 100;        // |exponent| of a scale
+constexpr int kRowThreads = 256;         // 8 warps = 8 rows per CTA and pass
+constexpr int kRowWarps = kRowThreads / 32;
+
+struct QCacheView {
+  uint8_t* codes;        // E4M3 [B, max_len, d_latent]
+  float* scales;         // fp32 [B, max_len, ceil(d_latent / 128)]
+  __nv_bfloat16* rope;   // bf16 [B, max_len, d_rope]
+};
+
+// ------------------------------------------------------------------------- conversions
+// Largest finite magnitude of two packed bf16, as bit patterns (they order like the magnitudes).
+__device__ __forceinline__ uint32_t finite_mag2(uint32_t v) {
+  uint32_t m = v & 0x7FFF7FFFu;
+  if ((m & 0xFFFFu) >= 0x7F80u) m &= 0xFFFF0000u;
+  if ((m >> 16) >= 0x7F80u) m &= 0x0000FFFFu;
+  return m;
+}
+__device__ __forceinline__ bool has_nan2(uint32_t v) {
+  return (v & 0x7FFFu) > 0x7F80u || ((v >> 16) & 0x7FFFu) > 0x7F80u;
+}
+// Exponent of the scale from the bf16 bit pattern of amax: 448 = 1.75 * 2^8, so the smallest e
+// is (exponent of amax) - 8, one more where amax's significand is above 1.75 (mantissa 0x60).
+// Subnormal magnitudes end at the lower bound either way.
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
+  if (amax_bits == 0) return 0;
+  const int e = static_cast<int>(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7Fu) > 0x60u ? 1 : 0);
+  return max(-kScaleExpMax, min(kScaleExpMax, e));
+}
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// Two packed bf16 times `inv`, rounded to E4M3 (to nearest even, magnitudes held to 448).
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t v, float inv) {
+  const float lo = __uint_as_float(v << 16) * inv, hi = __uint_as_float(v & 0xFFFF0000u) * inv;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, float inv) {
+  return e4m3x2(a, inv) | (e4m3x2(b, inv) << 16);
+}
+
+// E4M3 codes as bf16 without a conversion instruction: sign, exponent and mantissa of the code
+// are moved to where bf16 has them, which is the code's value times 2^-120 (bf16's bias is 127,
+// E4M3's 7), subnormals included. A product with 2^120 * scale then gives the value exactly.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+struct Dequant {
+  uint32_t f;            // bf16x2: 2^120 * scale, or 2^120 where that would overflow
+  uint32_t f2;           // bf16x2: scale, used in that case only
+  bool two;
+  __device__ __forceinline__ explicit Dequant(float scale) {
+    two = scale > 128.0f;                                  // 2^120 * 2^8 is not a bf16
+    const uint32_t hi = __float_as_uint(two ? 0x1p120f : scale * 0x1p120f) >> 16;
+    f = hi | (hi << 16);
+    const uint32_t s = __float_as_uint(scale) >> 16;
+    f2 = s | (s << 16);
+  }
+  __device__ __forceinline__ uint32_t pair(uint32_t t) const {      // t: codes in bytes 1 and 3
+    const uint32_t r = ((t & 0x7F007F00u) >> 4) | (t & 0x80008000u);
+    return mul_bf16x2(r, f);
+  }
+  // 4 codes -> 4 bf16
+  __device__ __forceinline__ uint2 operator()(uint32_t w) const {
+    return make_uint2(pair(__byte_perm(w, 0u, 0x1404)), pair(__byte_perm(w, 0u, 0x3424)));
+  }
+  // 16 codes -> 16 bf16
+  __device__ __forceinline__ void operator()(const uint4& c, uint4& lo, uint4& hi) const {
+    const uint2 a = (*this)(c.x), b = (*this)(c.y), d = (*this)(c.z), e = (*this)(c.w);
+    lo = make_uint4(a.x, a.y, b.x, b.y);
+    hi = make_uint4(d.x, d.y, e.x, e.y);
+    if (two) {
+      lo = make_uint4(mul_bf16x2(lo.x, f2), mul_bf16x2(lo.y, f2), mul_bf16x2(lo.z, f2), mul_bf16x2(lo.w, f2));
+      hi = make_uint4(mul_bf16x2(hi.x, f2), mul_bf16x2(hi.y, f2), mul_bf16x2(hi.z, f2), mul_bf16x2(hi.w, f2));
+    }
+  }
+};
+
+// ------------------------------------------------------------------------- write
+struct QCacheWriteParams {
+  const __nv_bfloat16* latent;   // [B, n_src, d_latent + d_rope], or null
+  const __nv_bfloat16* keys;     // [B, n_src, idx_dim], or null
+  const int32_t* src;            // [B, n] source row of each written row (< 0: none), or null: row j
+  const int32_t* start;          // [B] position of the first written row, or null: 0
+  const int32_t* lengths;        // [B] end of each sequence, or null: max_len
+  QCacheView cache;
+  uint8_t* k_idx;                // E4M3 [B, max_len, idx_dim]
+  float* k_scale;                // fp32 [B, max_len]
+  uint32_t* status;
+  int32_t n, n_src, max_len, d_latent, d_rope, idx_dim;
+  int64_t rows;                  // B * n
+};
+
+__device__ __forceinline__ uint32_t group_max(uint32_t m, int width) {
+  for (int o = width >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+__global__ void __launch_bounds__(kRowThreads) qcache_write_kernel(const QCacheWriteParams p) {
+  const uint32_t lane = lane_id();
+  const int groups = (p.d_latent + kScaleGroup - 1) / kScaleGroup;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp_id(); row < p.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const int64_t b = row / p.n;
+    const int32_t j = static_cast<int32_t>(row - b * p.n);
+    const int32_t s = p.src != nullptr ? __ldg(p.src + row) : j;
+    const int64_t pos = (p.start != nullptr ? static_cast<int64_t>(__ldg(p.start + b)) : 0) + j;
+    const int64_t end = p.lengths != nullptr ? static_cast<int64_t>(__ldg(p.lengths + b)) : p.max_len;
+    if (s < 0 || pos < 0 || (p.lengths != nullptr && pos >= end)) continue;
+    if (s >= p.n_src || pos >= p.max_len) {
+      if (lane == 0) record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(row));
+      continue;
+    }
+    const int64_t from = b * p.n_src + s, to = b * p.max_len + pos;
+    // every load of the row first
+    uint4 a0 = zero, a1 = zero, r = zero, k = zero;
+    const bool has_lat = p.latent != nullptr && static_cast<int32_t>(16 * lane) < p.d_latent;
+    const bool has_rope = p.latent != nullptr && static_cast<int32_t>(8 * lane) < p.d_rope;
+    const bool has_key = p.keys != nullptr && static_cast<int32_t>(8 * lane) < p.idx_dim;
+    const __nv_bfloat16* lat = p.latent + from * (p.d_latent + p.d_rope);
+    if (has_lat) {
+      const uint4* x = reinterpret_cast<const uint4*>(lat + 16 * lane);
+      a0 = __ldg(x);
+      a1 = __ldg(x + 1);
+    }
+    if (has_rope) r = __ldg(reinterpret_cast<const uint4*>(lat + p.d_latent + 8 * lane));
+    if (has_key) k = __ldg(reinterpret_cast<const uint4*>(p.keys + from * p.idx_dim + 8 * lane));
+    if (p.latent != nullptr) {
+      // 8 lanes hold a group of 128
+      uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(finite_mag2(a0.x), finite_mag2(a0.y)),
+                                     __vmaxu2(finite_mag2(a0.z), finite_mag2(a0.w))),
+                            __vmaxu2(__vmaxu2(finite_mag2(a1.x), finite_mag2(a1.y)),
+                                     __vmaxu2(finite_mag2(a1.z), finite_mag2(a1.w))));
+      const bool nan = has_nan2(a0.x) || has_nan2(a0.y) || has_nan2(a0.z) || has_nan2(a0.w) || has_nan2(a1.x) ||
+                       has_nan2(a1.y) || has_nan2(a1.z) || has_nan2(a1.w);
+      const uint32_t nans = __ballot_sync(0xffffffffu, nan);
+      const int e = scale_exp(group_max(max(m & 0xFFFFu, m >> 16), 8));
+      const float inv = pow2f(-e);
+      if (has_lat) {
+        reinterpret_cast<uint4*>(p.cache.codes + to * p.d_latent)[lane] =
+            make_uint4(e4m3x4(a0.x, a0.y, inv), e4m3x4(a0.z, a0.w, inv), e4m3x4(a1.x, a1.y, inv),
+                       e4m3x4(a1.z, a1.w, inv));
+        if ((lane & 7u) == 0)
+          p.cache.scales[to * groups + (lane >> 3)] = ((nans >> lane) & 0xFFu) ? __int_as_float(0x7FC00000) : pow2f(e);
+      }
+      if (has_rope) reinterpret_cast<uint4*>(p.cache.rope + to * p.d_rope)[lane] = r;
+    }
+    if (p.keys != nullptr) {
+      // 16 lanes hold the key (idx_dim <= 128)
+      const uint32_t m = __vmaxu2(__vmaxu2(finite_mag2(k.x), finite_mag2(k.y)),
+                                  __vmaxu2(finite_mag2(k.z), finite_mag2(k.w)));
+      const int e = scale_exp(group_max(max(m & 0xFFFFu, m >> 16), 16));
+      const float inv = pow2f(-e);
+      if (has_key)
+        reinterpret_cast<uint2*>(p.k_idx + to * p.idx_dim)[lane] =
+            make_uint2(e4m3x4(k.x, k.y, inv), e4m3x4(k.z, k.w, inv));
+      if (lane == 0) p.k_scale[to] = pow2f(e);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- read
+struct QCacheReadParams {
+  QCacheView cache;
+  const int32_t* listed;         // [B, n] positions (< 0: a zero row), or null: start[b] + j
+  const int32_t* start;          // [B], or null: 0
+  const int32_t* lengths;        // [B], or null: max_len
+  __nv_bfloat16* out;            // [B, n, d_latent + d_rope]
+  uint32_t* status;
+  int32_t n, max_len, d_latent, d_rope;
+  int64_t rows;                  // B * n
+};
+
+__global__ void __launch_bounds__(kRowThreads) qcache_read_kernel(const QCacheReadParams p) {
+  const uint32_t lane = lane_id();
+  const int groups = (p.d_latent + kScaleGroup - 1) / kScaleGroup;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp_id(); row < p.rows;
+       row += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const int64_t b = row / p.n;
+    int64_t pos;
+    bool ok;
+    if (p.listed != nullptr) {
+      pos = __ldg(p.listed + row);
+      ok = pos >= 0 && pos < p.max_len;
+      if (pos >= p.max_len && lane == 0) record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(row));
+    } else {
+      pos = (p.start != nullptr ? static_cast<int64_t>(__ldg(p.start + b)) : 0) + (row - b * p.n);
+      const int64_t end = p.lengths != nullptr ? static_cast<int64_t>(__ldg(p.lengths + b)) : p.max_len;
+      ok = pos >= 0 && pos < end && pos < p.max_len;
+    }
+    const int64_t at = b * p.max_len + pos;
+    const bool has_lat = static_cast<int32_t>(16 * lane) < p.d_latent;
+    const bool has_rope = static_cast<int32_t>(8 * lane) < p.d_rope;
+    uint4 c = zero, r = zero;
+    float s = 0.f;
+    if (ok && has_lat) {
+      c = __ldg(reinterpret_cast<const uint4*>(p.cache.codes + at * p.d_latent) + lane);
+      s = __ldg(p.cache.scales + at * groups + (lane >> 3));
+    }
+    if (ok && has_rope) r = __ldg(reinterpret_cast<const uint4*>(p.cache.rope + at * p.d_rope) + lane);
+    __nv_bfloat16* dst = p.out + row * (p.d_latent + p.d_rope);
+    if (has_lat) {
+      uint4 lo, hi;
+      const Dequant expand(s);
+      expand(c, lo, hi);
+      uint4* o = reinterpret_cast<uint4*>(dst + 16 * lane);
+      o[0] = lo;
+      o[1] = hi;
+    }
+    if (has_rope) reinterpret_cast<uint4*>(dst + p.d_latent)[lane] = r;
+  }
+}
+
+}  // namespace dsa
