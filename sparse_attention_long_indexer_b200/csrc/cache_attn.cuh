@@ -7,33 +7,37 @@
 // S_t is the query's list of cache positions; with a tree, query i of a sequence is node i of its
 // drafted tokens, and S_t also holds the drafted rows on node i's path (itself, its parent, ...).
 //
-// Work split. One CTA owns 128 heads x 256 output dims of one query over a range of its rows: the
-// fp32 output (256 TMEM columns) leaves room for two 64-row logits buffers (128 columns) and 256
-// dims of q (128 columns). The two halves of a query are independent CTAs that both compute the
-// logits: no exchange and no cluster, every product a full-rate M = 128 one-SM tcgen05 MMA, at
-// the price of reading the rows twice (from L2, half the bytes of a bf16 row each time).
-// When there are fewer (query, half) pairs than SMs, a query's rows are also split into ranges
-// whose normalised fp32 outputs and log-sum-exps are joined by cache_attn_join_kernel.
+// Work split. A pair of CTAs (a 2-CTA cluster) takes one query over a range of its rows, with 2-SM
+// tcgen05 MMAs issued by the even CTA: the fp32 output of 128 heads x 512 dims fills one SM's tensor
+// memory, so each CTA holds 64 heads. Per 64-row block,
+//  * logits: M = 128 heads (64 per CTA), N = 64 rows (CTA r supplies rows 32r ..), K = all dims;
+//  * output: M = 128 heads, N = 256 dims per instruction (CTA r supplies dims 256i + 128r ..),
+//    K = 64 rows, A = P from shared memory.
+// When there are fewer queries than pairs, a query's rows are split into ranges whose normalised
+// fp32 outputs and log-sum-exps are joined by cache_attn_join_kernel. (One CTA per 256 output dims,
+// which needs no cluster but computes and expands everything for the logits twice, took 1.67 ms for
+// 1024 queries of 2048 rows.)
 //
-// One CTA, 13 warps:
-//  * producers (8 warps): 64-row blocks into a 2-stage ring of 128-byte-swizzled bf16 tiles. 8-bit
-//    rows are loaded into registers one block ahead, so the gather's latency overlaps the previous
-//    block, and expanded to bf16 on the way to shared memory (exact: see qcache.cuh). bf16 rows
-//    (drafted rows, bf16 cache) are copied with cp.async. Rows that are not attended (padding, out
-//    of range, off the path) are zero rows, so nothing they hold in memory reaches a product.
-//  * MMA (1 thread): logits of block b+1, then output of block b. Logits: M = 128 heads, N = 64
-//    rows, A = q (dims 0..255 from TMEM, the rest from shared memory). Output: A = P from TMEM (it
-//    overwrites the block's logits), B = the same tile's first dims, N = 256.
-//  * softmax (4 warps, one thread per head): online softmax in the log2 domain. The running max is
-//    raised, and the output rescaled, only when it grows by more than kLazyRescale.
+// One CTA, 22 warps:
+//  * producers: 8 warps bring this CTA's 32 rows of each block, all dims (the logits' operand), 8 warps
+//    all 64 rows' dims that it supplies to the output; each part has a 2-stage ring of
+//    128-byte-swizzled bf16 tiles. 8-bit rows are loaded into registers one block ahead and expanded
+//    to bf16 on the way to shared memory (exact: see qcache.cuh). Shared memory stays below 196 KB
+//    on purpose: the L1 keeps 60 KB, which is what loads in flight land in. bf16 rows (drafted rows,
+//    bf16 cache) are copied with cp.async. Rows that are not attended (padding, out of range, off
+//    the path) are zero rows, so nothing they hold in memory reaches a product.
+//  * MMA: one warp issues the logits, one the outputs (even CTA).
+//  * softmax: 4 warps; lane L has rows 32 (L / 64) .. +31 of a block of head L % 64 of this CTA.
+//    Online softmax in the log2 domain; the running max is raised, and the output rescaled, only when
+//    it grows by more than kLazyRescale.
 // Statistics and outputs are fp32; P is rounded to bf16 for the tensor core. The output is
 // normalised by the sum of the rounded weights (so they add up to one), lse takes the unrounded.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
 
-#include "qcache.cuh"
 #include "ptx.cuh"
+#include "qcache.cuh"
 #include "sparse_mla.cuh"
 
 namespace dsa {
@@ -42,32 +46,38 @@ constexpr int kMaxDraft = 256;           // nodes of a drafted tree
 
 struct CacheAttnCfg {
   static constexpr int BLK = 64;                         // rows per block
-  static constexpr int STAGES = 2;
-  static constexpr int ATOM = BLK * 128;                 // 64 rows x 64 dims
-  static constexpr int STAGE_BYTES = 9 * ATOM;           // 64 rows x 576 dims
-  static constexpr int Q_TMEM_DIMS = 256;
-  static constexpr int Q_ATOM = kHeads * 128;            // 128 heads x 64 dims
+  static constexpr int L_ATOM = 32 * 128;                // logits part: 32 rows x 64 dims
+  static constexpr int L_BYTES = 9 * L_ATOM;             // 32 rows x 576 dims
+  static constexpr int O_ATOM = BLK * 128;               // output part: 64 rows x 64 dims
+  static constexpr int O_BYTES = 4 * O_ATOM;             // 64 rows x 256 dims
+  static constexpr int Q_TMEM_DIMS = 320;
+  static constexpr int Q_ATOM = 64 * 128;                // 64 heads x 64 dims
   static constexpr int QS_ATOMS = (kDqk - Q_TMEM_DIMS) / 64;
+  static constexpr int P_BYTES = 64 * 128;               // 64 heads x 64 rows bf16
+  static constexpr int S_BUFS = 3;                       // TMEM logits buffers, 32 columns each
   static constexpr int SOFTMAX_WARPS = 4;
-  static constexpr int PRODUCER_WARPS = 8;
-  static constexpr int ROWS = BLK / PRODUCER_WARPS;      // rows of a block per producer warp
-  static constexpr int MMA_WARP = SOFTMAX_WARPS + PRODUCER_WARPS;
-  static constexpr int THREADS = (MMA_WARP + 1) * 32;
-  static constexpr int OUT_DIMS = 256;                   // output dims per CTA
+  static constexpr int PART_WARPS = 8;                   // producer warps per part
+  static constexpr int PRODUCER_WARPS = 2 * PART_WARPS;
+  static constexpr int S_WARP = SOFTMAX_WARPS + PRODUCER_WARPS;   // logits MMAs (and TMEM owner)
+  static constexpr int O_WARP = S_WARP + 1;                       // output MMAs
+  static constexpr int THREADS = (O_WARP + 1) * 32;
   // TMEM columns
-  static constexpr uint32_t COL_O = 0, COL_S = 256, COL_Q = COL_S + 2 * BLK, TMEM_COLS = 512;
+  static constexpr uint32_t COL_O = 0, COL_S = 256, COL_Q = COL_S + 32 * S_BUFS, TMEM_COLS = 512;
   // shared memory
-  static constexpr int OFF_STAGE = 0;
-  static constexpr int OFF_QS = OFF_STAGE + STAGES * STAGE_BYTES;
-  static constexpr int OFF_INFO = OFF_QS + QS_ATOMS * Q_ATOM;
+  static constexpr int OFF_L = 0;                        // 2 stages
+  static constexpr int OFF_O = OFF_L + 2 * L_BYTES;      // 2 stages
+  static constexpr int OFF_QS = OFF_O + 2 * O_BYTES;
+  static constexpr int OFF_P = OFF_QS + QS_ATOMS * Q_ATOM;         // 2 buffers
+  static constexpr int OFF_XCHG = OFF_P + 2 * P_BYTES;             // [2][128] tagged words
+  static constexpr int OFF_INFO = OFF_XCHG + 2 * 128 * 8;
   static constexpr int INFO_WORDS = 4 + kMaxDraft / 32;  // list blocks, list end, tail blocks, first tail block, path
   static constexpr int OFF_BAR = OFF_INFO + 2 * INFO_WORDS * 4;
-  static constexpr int NUM_BARS = 17;
+  static constexpr int NUM_BARS = 26;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-  static_assert(STAGE_BYTES % 1024 == 0 && OFF_QS % 1024 == 0 && OFF_BAR % 8 == 0, "layout");
+  static_assert(OFF_O % 1024 == 0 && OFF_QS % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "layout");
   static_assert(COL_Q + Q_TMEM_DIMS / 2 <= TMEM_COLS, "TMEM");
-  static_assert(SMEM_BYTES <= 232448, "shared memory");
+  static_assert(SMEM_BYTES <= 195 * 1024, "leaves the L1 its 60 KB");
 };
 
 struct CacheAttnParams {
@@ -83,26 +93,102 @@ struct CacheAttnParams {
   float* part_lse;               // [T, n_splits, n_heads], log2 domain
   uint32_t* status;
   int32_t n_q, max_len, topk, n_heads, d_latent, d_rope;
-  int32_t n_halves, n_splits, split_blocks, n_items;
+  int32_t n_splits, split_blocks, n_items;
   float scale_log2;              // tau * log2(e), positive
   uint64_t wait_budget_ns;
 };
 
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16 -> f32, one SM.
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Arrives once on the barrier at this offset in both CTAs of the pair when every 2-SM MMA this thread
+// has issued so far is done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
       : "memory");
+}
+// True in one lane of a converged warp (always the same one). The whole warp walks the MMA role's code
+// and one lane, elected right at the instructions, issues them: the operands then stay in uniform
+// registers, where the instructions want them. Issued from inside `if (lane == 0)` an MMA cost 90 to
+// 250 clocks.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// Loads that stay where they are written (volatile): the producers issue a block's loads one block
+// before their use, and a load that the compiler may move is moved down to its use. Zero without `in`.
+__device__ __forceinline__ uint4 ld_ahead_v4(const void* src, bool in) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(src), "r"(static_cast<uint32_t>(in)));
+  return v;
+}
+__device__ __forceinline__ float ld_ahead_f32(const float* src, bool in) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0f00000000;\n\t"
+      "@p ld.global.nc.f32 %0, [%1];\n\t}"
+      : "=&f"(v)
+      : "l"(src), "r"(static_cast<uint32_t>(in)));
+  return v;
+}
+
+// Bounded waits on the SM's own clock. (The wait of ptx.cuh takes its time from %globaltimer, whose
+// first read, about a thousand clocks, every wait that is not over at once would pay.) Same contract:
+// past the budget the error is recorded and the CTA's abort flag raised, and every later wait fails.
+struct ClockWaiter {
+  uint32_t* status;
+  volatile int* abort;
+  int64_t budget;            // clocks
+  __device__ __forceinline__ bool aborted() const { return *abort != 0; }
+  // One more unsuccessful try: false once the CTA has aborted or the budget is spent.
+  __device__ __forceinline__ bool again(uint32_t& spins, int64_t& t0, uint32_t tag) const {
+    if ((++spins & 63u) != 0) return true;
+    if (*abort) return false;
+    if (t0 == 0) {
+      t0 = clock64();
+      return true;
+    }
+    if (clock64() - t0 <= budget) return true;
+    record_error(status, DSA_ERR_DEVICE_TIMEOUT, (4u << 16) | tag);
+    *abort = 1;
+    __threadfence_block();
+    return false;
+  }
+  // kCluster: some of the barrier's arrivals come from the other CTA of the pair
+  template <bool kCluster = false>
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t tag) const {
+    uint32_t spins = 0;
+    int64_t t0 = 0;
+    while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
+      if (!again(spins, t0, tag)) return false;
+    return true;
+  }
+  // The low half of the 64-bit shared word at `addr` once its high half is `number` (one aligned store
+  // writes both, so the pair is seen whole).
+  __device__ __forceinline__ bool wait_word(uint32_t addr, uint32_t number, uint32_t tag, uint32_t& value) const {
+    uint32_t spins = 0;
+    int64_t t0 = 0;
+    while (true) {
+      uint64_t w;
+      asm volatile("ld.volatile.shared.u64 %0, [%1];" : "=l"(w) : "r"(addr) : "memory");
+      value = static_cast<uint32_t>(w);
+      if (static_cast<uint32_t>(w >> 32) == number) return true;
+      if (!again(spins, t0, tag)) return false;
+    }
+  }
+};
+
 template <bool kQuant, bool kTree>
-__global__ void __launch_bounds__(CacheAttnCfg::THREADS, 1)
+__global__ void __launch_bounds__(CacheAttnCfg::THREADS, 1) __cluster_dims__(2, 1, 1)
 cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnParams p) {
   using C = CacheAttnCfg;
   extern __shared__ uint8_t smem_raw[];
@@ -111,66 +197,97 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   volatile int32_t* info_base = reinterpret_cast<volatile int32_t*>(smem + C::OFF_INFO);
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto B = [&](uint32_t i) { return bar0 + 8u * i; };
-  auto full = [&](uint32_t s) { return B(0 + s); };          // producer warps: a block's tile is in shared memory
-  auto empty = [&](uint32_t s) { return B(2 + s); };         // commit: the block's output MMAs are done
-  auto s_full = [&](uint32_t s) { return B(4 + s); };        // commit: logits ready
-  auto p_full = [&](uint32_t s) { return B(6 + s); };        // softmax warps: P written
-  auto info_full = [&](uint32_t i) { return B(8 + i); };     // first producer warp
-  auto info_empty = [&](uint32_t i) { return B(10 + i); };   // everyone who reads info
-  const uint32_t q_full = B(12);                             // producer warps + TMA
-  const uint32_t q_empty = B(13);                            // commit: the item's logits MMAs are done
-  const uint32_t o_full = B(14);                             // commit: the item's output MMAs are done
-  const uint32_t o_empty = B(15);                            // softmax warps: output read
-  const uint32_t mma_done = B(16);
+  // in both CTAs
+  auto info_full = [&](uint32_t i) { return B(0 + i); };     // first producer warp
+  auto info_empty = [&](uint32_t i) { return B(2 + i); };    // everyone else who reads info
+  auto s_full = [&](uint32_t i) { return B(4 + i); };        // commit (3): logits of a block done, its part read
+  auto o_done = [&](uint32_t j) { return B(7 + j); };        // commit (2): outputs of a block done, its part and P read
+  const uint32_t o_full = B(9);                              // commit: the item's outputs are done
+  const uint32_t q_empty = B(10);                            // commit: the item's logits are done
+  const uint32_t q_tma = B(11);                              // this CTA's part of q in shared memory has landed
+  auto p_local = [&](uint32_t j) { return B(12 + j); };      // odd CTA's softmax warps: P written
+  // in the even CTA, arrived on by both
+  auto l_full = [&](uint32_t s) { return B(14 + s); };       // producer warps: a logits part is in
+  auto v_full = [&](uint32_t s) { return B(16 + s); };       // producer warps: an output part is in
+  const uint32_t q_full = B(18);                             // producer warps and the TMA part
+  auto p_full = [&](uint32_t j) { return B(19 + j); };       // its softmax warps, and the odd CTA's relay
+  const uint32_t o_empty = B(21);                            // softmax warps: outputs read
+  // in the even CTA only: a logits buffer is free, once the output warp has seen its block's P
+  auto s_free = [&](uint32_t i) { return B(22 + i); };       // (3)
+  const uint32_t mma_done = B(25);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
   const uint32_t warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
   if (threadIdx.x == 0) {
-    for (uint32_t s = 0; s < 2; ++s) {
-      mbar_init(full(s), C::PRODUCER_WARPS);
-      mbar_init(empty(s), 1);
-      mbar_init(s_full(s), 1);
-      mbar_init(p_full(s), C::SOFTMAX_WARPS);
-      mbar_init(info_full(s), 1);
-      mbar_init(info_empty(s), C::SOFTMAX_WARPS + (C::PRODUCER_WARPS - 1) + 1);
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(info_full(i), 1);
+      // softmax and producer warps (without the first), and the MMA warps (odd CTA: the relay)
+      mbar_init(info_empty(i), C::SOFTMAX_WARPS + C::PRODUCER_WARPS - 1 + (leader ? 2 : 1));
+      mbar_init(o_done(i), 1);
+      mbar_init(p_local(i), C::SOFTMAX_WARPS);
+      mbar_init(l_full(i), 2 * C::PART_WARPS);
+      mbar_init(v_full(i), 2 * C::PART_WARPS);
+      mbar_init(p_full(i), C::SOFTMAX_WARPS + 1);
     }
-    mbar_init(q_full, C::PRODUCER_WARPS + 1);
-    mbar_init(q_empty, 1);
+    for (uint32_t i = 0; i < static_cast<uint32_t>(C::S_BUFS); ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(s_free(i), 1);
+    }
     mbar_init(o_full, 1);
-    mbar_init(o_empty, C::SOFTMAX_WARPS);
-    mbar_init(mma_done, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(q_tma, 1);
+    mbar_init(q_full, 2 * (C::PART_WARPS + 1));
+    mbar_init(o_empty, 2 * C::SOFTMAX_WARPS);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == C::MMA_WARP) {
-    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
-    tmem_relinquish();
+  // exchange numbers start at 1
+  for (uint32_t i = threadIdx.x; i < 256u; i += C::THREADS) reinterpret_cast<uint64_t*>(smem + C::OFF_XCHG)[i] = 0;
+  if (warp == C::S_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(C::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();            // both CTAs' barriers and TMEM exist before any remote traffic
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Waiter wt{p.status, abort_flag, p.wait_budget_ns, 4u};
+  const ClockWaiter wt{p.status, abort_flag, static_cast<int64_t>(p.wait_budget_ns) * 2};   // at most 2 clocks per ns
+  const int32_t n_pairs = static_cast<int32_t>(nclusters_x());
+  const int32_t pair = static_cast<int32_t>(cluster_id_x());
+  const uint32_t lead_off = mapa(bar0, 0) - bar0;            // the even CTA's copy of a barrier
+  // arrives on the even CTA's copy of a barrier: across the pair only from the odd CTA
+  auto arrive_leader = [&](uint32_t bar) {
+    if (leader) mbar_arrive(bar);
+    else mbar_arrive_cluster(bar + lead_off);
+  };
   auto warp_wait = [&](uint32_t bar, uint32_t parity, uint32_t tag) -> bool {
     uint32_t got = 1;
     if (lane == 0) got = wt.wait(bar, parity, tag) ? 1u : 0u;
     return __shfl_sync(0xffffffffu, got, 0) != 0;
   };
+  auto warp_wait_pair = [&](uint32_t bar, uint32_t parity, uint32_t tag) -> bool {
+    uint32_t got = 1;
+    if (lane == 0) got = wt.template wait<true>(bar, parity, tag) ? 1u : 0u;
+    return __shfl_sync(0xffffffffu, got, 0) != 0;
+  };
 
-  // item -> (query, range of its rows, half of the output dims); the halves of a query are
-  // neighbours, so that the rows one reads are in L2 for the other
+  // item -> (query, range of its rows)
   struct Item {
-    int32_t qi, split, half;
+    int32_t qi, split;
     int32_t e0, e1;       // list entries of the range
     int32_t k0, k1;       // 64-row blocks of drafted rows of the range
   };
   auto item_of = [&](int32_t it) {
     Item m;
-    m.half = it % p.n_halves;
-    const int32_t rest = it / p.n_halves;
-    m.split = rest % p.n_splits;
-    m.qi = rest / p.n_splits;
+    m.split = it % p.n_splits;
+    m.qi = it / p.n_splits;
     const int32_t list_blocks = (p.topk + C::BLK - 1) / C::BLK;
     const int32_t all_blocks = list_blocks + (kTree ? (p.n_q + C::BLK - 1) / C::BLK : 0);
     const int32_t b0 = m.split * p.split_blocks, b1 = min(b0 + p.split_blocks, all_blocks);
@@ -181,13 +298,35 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     return m;
   };
   const int32_t d_qk = p.d_latent + p.d_rope;
+  const int32_t k_steps = (d_qk + 15) / 16;
 
-  if (warp >= static_cast<uint32_t>(C::SOFTMAX_WARPS) && warp < static_cast<uint32_t>(C::MMA_WARP)) {
+  if (warp >= static_cast<uint32_t>(C::SOFTMAX_WARPS) && warp < static_cast<uint32_t>(C::S_WARP)) {
     // ================================================================ producers
-    const uint32_t pw = warp - C::SOFTMAX_WARPS;        // rows ROWS*pw .. of every block
-    uint32_t n_it = 0, n_q_loads = 0, nb = 0;           // items, items with blocks, blocks so far
+    const uint32_t pw = warp - C::SOFTMAX_WARPS;
+    const bool logits_part = pw < static_cast<uint32_t>(C::PART_WARPS);
+    const uint32_t gt = (pw % C::PART_WARPS) * 32u + lane;   // thread of the part, 0..255
+    // Logits part: eight threads per row, thread c has the row's 16-dim pieces c, c + 8, ...: one per
+    // scale group. Output part: four threads per row, thread c has piece c of each of the four atoms.
+    // A store instruction of eight threads then covers eight 16-byte chunks in distinct bank groups
+    // (logits part: two atoms, so the threads of the second store their two chunks in opposite order).
+    const uint32_t row = logits_part ? gt >> 3 : gt >> 2;    // row of the part's tile
+    const uint32_t c = logits_part ? gt & 7u : gt & 3u;
+    const uint32_t row_at = (row >> 3) * 1024u + (row & 7u) * 128u;
+    const uint32_t at0 = row_at + (((2 * (c & 3u)) ^ (row & 7u)) << 4);
+    const uint32_t at1 = row_at + (((2 * (c & 3u) + 1) ^ (row & 7u)) << 4);
+    const bool swap = logits_part && (c & 4u) != 0;
+    const int32_t block_row = static_cast<int32_t>(row + (logits_part ? 32u * rank : 0u));   // row of the block
+    // piece k of this thread: its first dim, and where it goes in the tile
+    auto piece_dim = [&](int32_t k) -> int32_t {
+      return logits_part ? 16 * (static_cast<int32_t>(c) + 8 * k)
+                         : 256 * (k >> 1) + 128 * static_cast<int32_t>(rank) + 64 * (k & 1) + 16 * static_cast<int32_t>(c);
+    };
+    auto piece_at = [&](int32_t k) -> uint32_t {
+      return logits_part ? (2u * k + (c >> 2)) * C::L_ATOM : static_cast<uint32_t>(k) * C::O_ATOM;
+    };
+    uint32_t n_it = 0, n_busy = 0, nb = 0;                   // items, items with blocks, blocks so far
     bool tma_pending = false;
-    for (int32_t it = blockIdx.x; it < p.n_items; it += gridDim.x, ++n_it) {
+    for (int32_t it = pair; it < p.n_items; it += n_pairs, ++n_it) {
       const Item m = item_of(it);
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
       volatile int32_t* info = info_base + slot * C::INFO_WORDS;
@@ -254,315 +393,357 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         if (!warp_wait(info_full(slot), sph, 2)) break;
       }
       const int32_t n_list = info[0], end = info[1], n_tail = info[2], k0 = info[3];
-      uint64_t path = 0;                                 // this warp's rows of a drafted block, by block
+      uint32_t path = 0;                                 // bit k: this thread's row of drafted block k0 + k is attended
       if constexpr (kTree) {
-        // byte k of `path`: rows ROWS*pw .. +7 of drafted block k0 + k (at most 4 blocks)
-        for (int32_t k = 0; k < n_tail; ++k) {
-          const uint32_t w = static_cast<uint32_t>(info[4 + 2 * (k0 + k) + (pw >> 2)]);
-          path |= static_cast<uint64_t>((w >> (8 * (pw & 3u))) & 0xFFu) << (8 * k);
-        }
+        for (int32_t k = 0; k < n_tail; ++k)
+          path |= ((static_cast<uint32_t>(info[4 + 2 * (k0 + k) + (block_row >> 5)]) >> (block_row & 31)) & 1u) << k;
       }
       __syncwarp();
       if (pw != 0 && lane == 0) mbar_arrive(info_empty(slot));
       if (n_list + n_tail == 0) continue;
 
-      // ---- q: dims 0..255 into this warp's TMEM lanes, the rest by TMA, once the previous item's
-      // logits MMAs have read theirs. Heads and dims past the query's own are zeros in TMEM; the TMA
-      // part past the last dim is zero-filled, and rows past the last head only reach unused lanes.
-      if (!warp_wait(q_empty, (n_q_loads & 1u) ^ 1u, 3)) break;
-      ++n_q_loads;
-      if (pw == 0 && lane == 0) {
+      if (logits_part) {
+        // ---- q: dims 0..319 into this warp's TMEM lanes (both lane halves hold this CTA's 64 heads), the
+        // rest by TMA, once the previous item's logits MMAs have read theirs. Heads and dims past the
+        // query's own are zeros in TMEM; the TMA part past the last dim is zero-filled, and rows past
+        // the last head only reach unused lanes.
+        if (!warp_wait(q_empty, (n_busy & 1u) ^ 1u, 3)) break;
         const int32_t atoms = (d_qk - C::Q_TMEM_DIMS + 63) / 64;
-        if (atoms > 0) {
-          mbar_expect_tx(q_full, static_cast<uint32_t>(atoms) * C::Q_ATOM);
+        if (pw == 0 && lane == 0 && atoms > 0) {
+          mbar_expect_tx(q_tma, static_cast<uint32_t>(atoms) * C::Q_ATOM);
           tma_pending = true;
           for (int32_t a = 0; a < atoms; ++a)
-            tma_load_3d(sbase + C::OFF_QS + a * C::Q_ATOM, &map_q, q_full, C::Q_TMEM_DIMS + 64 * a,
-                        m.qi * p.n_heads, 0);
-        } else {
-          mbar_arrive(q_full);
+            tma_load_3d(sbase + C::OFF_QS + a * C::Q_ATOM, &map_q, q_tma, C::Q_TMEM_DIMS + 64 * a,
+                        m.qi * p.n_heads + 64 * static_cast<int32_t>(rank), 0);
         }
-      }
-      {
         tc_fence_after();
-        const int32_t head = 32 * static_cast<int32_t>(warp & 3u) + static_cast<int32_t>(lane);
-        const int32_t dim0 = 128 * static_cast<int32_t>(pw >> 2);
+        const int32_t head = static_cast<int32_t>(64u * rank + ((32u * (warp & 3u) + lane) & 63u));
+        const int32_t dim0 = C::Q_TMEM_DIMS / 2 * static_cast<int32_t>(pw >> 2);
         const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(m.qi) * p.n_heads + head) * d_qk + dim0;
-        uint32_t r[4][16];
+#pragma unroll 1
+        for (int k = 0; k < C::Q_TMEM_DIMS / 2 / 32; ++k) {      // 16 columns (32 dims) at a time
+          uint32_t r[16];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const bool in = head < p.n_heads && dim0 + 8 * c < d_qk;
-          const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(qrow) + c) : make_uint4(0, 0, 0, 0);
-          r[c >> 2][4 * (c & 3) + 0] = u.x;
-          r[c >> 2][4 * (c & 3) + 1] = u.y;
-          r[c >> 2][4 * (c & 3) + 2] = u.z;
-          r[c >> 2][4 * (c & 3) + 3] = u.w;
+          for (int v = 0; v < 4; ++v) {
+            const bool in = head < p.n_heads && dim0 + 32 * k + 8 * v < d_qk;
+            const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(qrow) + 4 * k + v) : make_uint4(0, 0, 0, 0);
+            r[4 * v + 0] = u.x;
+            r[4 * v + 1] = u.y;
+            r[4 * v + 2] = u.z;
+            r[4 * v + 3] = u.w;
+          }
+          tmem_st16(tmem + ((32u * (warp & 3u)) << 16) + C::COL_Q + dim0 / 2 + 16 * k, r);
         }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_st16(tmem + ((32u * (warp & 3u)) << 16) + C::COL_Q + dim0 / 2 + 16 * c, r[c]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        if (lane == 0) {
+          arrive_leader(q_full);
+          if (pw == 0 && (atoms <= 0 || wt.wait(q_tma, n_busy & 1u, 4))) arrive_leader(q_full);
+        }
+        __syncwarp();
       }
+      ++n_busy;
 
-      // ---- the blocks. Row i of this warp is row ROWS*pw + i of the block; within a tile its 16-byte
-      // chunk c of dims 8c.. is at atom c / 8, swizzled by i.
-      const uint32_t row_off = C::OFF_STAGE + pw * 1024u;
-      auto chunk_at = [&](uint32_t st, uint32_t i, uint32_t c) {
-        return sbase + row_off + st * C::STAGE_BYTES + (c >> 3) * C::ATOM + i * 128u + (((c & 7u) ^ i) << 4);
+      // ---- the blocks
+      // waits for the part's stage of block nb, and gives it
+      auto acquire = [&](uint32_t& tile) -> bool {
+        const uint32_t st = nb & 1u;
+        if (logits_part) {                                 // last read by the logits of block nb - 2
+          tile = sbase + C::OFF_L + st * C::L_BYTES;
+          return nb < 2 || warp_wait(s_full((nb - 2) % C::S_BUFS), ((nb - 2) / C::S_BUFS) & 1u, 5);
+        }
+        tile = sbase + C::OFF_O + st * C::O_BYTES;
+        return warp_wait(o_done(st), ((nb >> 1) & 1u) ^ 1u, 6);
       };
-      const int32_t chunks = d_qk / 8, chunks_even = (chunks + 1) & ~1;   // a K step is two chunks
-      auto announce = [&](uint32_t st) {
+      auto announce = [&]() {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full(st));
+        if (lane == 0) arrive_leader(logits_part ? l_full(nb & 1u) : v_full(nb & 1u));
       };
-      // position of entry `lane` (< ROWS) of this warp in list block b, or -1
+      // this thread's entry of list block b (read ahead of its use), and the row it stands for, or -1
       auto entry = [&](int32_t b) -> int32_t {
-        const int32_t j = m.e0 + b * C::BLK + C::ROWS * static_cast<int32_t>(pw) + static_cast<int32_t>(lane);
-        if (b >= n_list || lane >= static_cast<uint32_t>(C::ROWS) || j >= end) return -1;
-        const int32_t v = __ldg(idx_row + j);
-        if (v >= p.max_len) {
-          record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(m.qi));
-          return -1;
-        }
-        return v < 0 ? -1 : v;
+        const int32_t j = m.e0 + b * C::BLK + block_row;
+        return b < n_list && j < end ? __ldg(idx_row + j) : -1;
       };
-      // ROWS bf16 rows of a table (row r_i, or zeros where r_i < 0) into a stage by cp.async
-      auto copy_rows = [&](uint32_t st, const __nv_bfloat16* table, int32_t rows) {
+      auto checked = [&](int32_t v) -> int32_t {
+        if (v < p.max_len) return v;
+        record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(m.qi));
+        return -1;
+      };
+      // one block of bf16 rows: row r of a table, zeros where r < 0
+      auto copy_block = [&](const __nv_bfloat16* table, int32_t r) -> bool {
+        const __nv_bfloat16* src = table + (r >= 0 ? static_cast<int64_t>(r) * d_qk : 0);
+        uint32_t tile;
+        if (!acquire(tile)) return false;
+        const int32_t dims = logits_part ? d_qk : p.d_latent;
 #pragma unroll
-        for (int i = 0; i < C::ROWS; ++i) {
-          const int32_t r = __shfl_sync(0xffffffffu, rows, i);
-          const __nv_bfloat16* src = table + (r >= 0 ? static_cast<size_t>(r) * d_qk : 0);
-          for (int32_t c = static_cast<int32_t>(lane); c < chunks_even; c += 32) {
-            const bool in = r >= 0 && c < chunks;
-            cp_async_16(chunk_at(st, i, c), src + (in ? 8 * c : 0), in ? 16u : 0u);
-          }
+        for (int32_t k = 0; k < 5; ++k) {
+          const int32_t d = piece_dim(k);
+          if ((k == 4 && !logits_part) || d >= dims) break;
+          const bool in0 = r >= 0, in1 = r >= 0 && d + 8 < d_qk;
+          cp_async_16(tile + piece_at(k) + at0, src + (in0 ? d : 0), in0 ? 16u : 0u);
+          cp_async_16(tile + piece_at(k) + at1, src + (in1 ? d + 8 : 0), in1 ? 16u : 0u);
         }
         cp_async_commit();
         cp_async_wait<0>();
+        announce();
+        return true;
       };
       bool ok = true;
       if constexpr (kQuant) {
         const int32_t groups = (p.d_latent + kScaleGroup - 1) / kScaleGroup;
-        const uint8_t* codes = p.cache.codes + seq * p.max_len * static_cast<int64_t>(p.d_latent) + 16 * lane;
-        const float* scales = p.cache.scales + seq * p.max_len * static_cast<int64_t>(groups) + (lane >> 3);
-        const __nv_bfloat16* rope = p.cache.rope + seq * p.max_len * static_cast<int64_t>(p.d_rope) + 8 * (lane & 7u);
-        const bool has_lat = static_cast<int32_t>(16 * lane) < p.d_latent;
-        const bool has_rope = static_cast<int32_t>(8 * (lane & 7u)) < p.d_rope;
-        const uint32_t lat_chunks = static_cast<uint32_t>(p.d_latent) / 8;
-        const uint32_t rope_chunk = lat_chunks + (lane & 7u);
-        // lanes of the two atoms that a store phase covers take their two chunks in opposite order,
-        // so the phase's eight 16-byte stores fall into distinct banks
-        const uint32_t swap = (lane >> 2) & 1u;
-        uint4 raw[C::ROWS], rp[2];
-        float sc[C::ROWS];
-        auto load_row = [&](int i, int32_t rows) {
-          const int32_t r = __shfl_sync(0xffffffffu, rows, i);
-          const bool in = r >= 0 && has_lat;
-          raw[i] = in ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<size_t>(r) * p.d_latent))
-                      : make_uint4(0, 0, 0, 0);
-          sc[i] = in ? __ldg(scales + static_cast<size_t>(r) * groups) : 0.f;
+        const uint8_t* codes = p.cache.codes + seq * p.max_len * static_cast<int64_t>(p.d_latent);
+        const float* scales = p.cache.scales + seq * p.max_len * static_cast<int64_t>(groups);
+        const __nv_bfloat16* rope = p.cache.rope + seq * p.max_len * static_cast<int64_t>(p.d_rope);
+        // Pieces below d_latent are codes, from there RoPE dims. Those are at most 64, so that a thread
+        // of the logits part has at most one such piece: piece rope_k, at RoPE dim rope_d.
+        const int32_t rope_k = (p.d_latent / 16 - static_cast<int32_t>(c) + 7) / 8;
+        const int32_t rope_d = piece_dim(rope_k) - p.d_latent;
+        const bool has_rope = logits_part && rope_d < p.d_rope;
+        uint4 raw[4], rp[2];
+        float sc[4];
+        auto load = [&](int32_t r) {
+          const uint8_t* src = codes + static_cast<int64_t>(r) * p.d_latent;
+          const float* s0 = scales + static_cast<int64_t>(r) * groups;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int32_t d = piece_dim(k);
+            const bool in = r >= 0 && d < p.d_latent;
+            raw[k] = ld_ahead_v4(src + d, in);
+            sc[k] = ld_ahead_f32(s0 + d / kScaleGroup, in);
+          }
+          if (has_rope) {
+            const __nv_bfloat16* rs = rope + static_cast<int64_t>(r) * p.d_rope + rope_d;
+            rp[0] = ld_ahead_v4(rs, r >= 0);
+            rp[1] = ld_ahead_v4(rs + 8, r >= 0 && rope_d + 8 < p.d_rope);
+          }
         };
-        auto load_rope = [&](int t, int32_t rows) {
-          const int32_t r = __shfl_sync(0xffffffffu, rows, 4 * t + (lane >> 3));
-          rp[t] = r >= 0 && has_rope ? __ldg(reinterpret_cast<const uint4*>(rope + static_cast<size_t>(r) * p.d_rope))
-                                     : make_uint4(0, 0, 0, 0);
-        };
-        int32_t rows = entry(0);
+        load(checked(entry(0)));
+        int32_t v = entry(1);
+        for (int32_t b = 0; b < n_list; ++b) {
+          // The next block's loads go out together after the announcement: a load among the uses of
+          // this block's would share a scoreboard with loads still to be used, which then wait for
+          // it, and the fence of the announcement waits for loads in flight.
+          uint32_t tile;
+          if (!acquire(tile)) { ok = false; break; }
 #pragma unroll
-        for (int i = 0; i < C::ROWS; ++i) load_row(i, rows);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) load_rope(t, rows);
-        rows = entry(1);
-        for (int32_t b = 0; b < n_list; ++b, ++nb) {
-          const uint32_t st = nb & 1u;
-          if (!warp_wait(empty(st), ((nb >> 1) & 1u) ^ 1u, 4)) { ok = false; break; }
-#pragma unroll
-          for (int i = 0; i < C::ROWS; ++i) {
+          for (int k = 0; k < 4; ++k) {
+            if (piece_dim(k) >= p.d_latent) break;
             uint4 lo, hi;
-            const Dequant expand(sc[i]);
-            expand(raw[i], lo, hi);
-            if (b + 1 < n_list) load_row(i, rows);
-            if (has_lat) {
-              st_shared_v4(chunk_at(st, i, 2 * lane + swap), swap ? hi : lo);
-              st_shared_v4(chunk_at(st, i, 2 * lane + (swap ^ 1u)), swap ? lo : hi);
-            }
+            const Dequant expand(sc[k]);
+            expand(raw[k], lo, hi);
+            st_shared_v4(tile + piece_at(k) + (swap ? at1 : at0), swap ? hi : lo);
+            st_shared_v4(tile + piece_at(k) + (swap ? at0 : at1), swap ? lo : hi);
           }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (static_cast<int32_t>(rope_chunk) < chunks_even)
-              st_shared_v4(chunk_at(st, 4 * t + (lane >> 3), rope_chunk), rp[t]);
-            if (b + 1 < n_list) load_rope(t, rows);
+          if (has_rope) {
+            st_shared_v4(tile + piece_at(rope_k) + at0, rp[0]);
+            st_shared_v4(tile + piece_at(rope_k) + at1, rp[1]);
           }
-          rows = entry(b + 2);
-          announce(st);
+          announce();
+          ++nb;
+          v = checked(v);
+          if (b + 1 < n_list) load(v);
+          v = entry(b + 2);
         }
       } else {
         const __nv_bfloat16* table = p.kv + seq * p.max_len * static_cast<int64_t>(d_qk);
-        int32_t rows = entry(0);
-        for (int32_t b = 0; b < n_list; ++b, ++nb) {
-          const uint32_t st = nb & 1u;
+        int32_t v = entry(0);
+        for (int32_t b = 0; b < n_list && ok; ++b, ++nb) {
           const int32_t next = entry(b + 1);
-          if (!warp_wait(empty(st), ((nb >> 1) & 1u) ^ 1u, 5)) { ok = false; break; }
-          copy_rows(st, table, rows);
-          rows = next;
-          announce(st);
+          ok = copy_block(table, checked(v));
+          v = next;
         }
       }
       if constexpr (kTree) {
         const __nv_bfloat16* table = p.draft + seq * p.n_q * static_cast<int64_t>(d_qk);
-        for (int32_t k = 0; k < n_tail && ok; ++k, ++nb) {
-          const uint32_t st = nb & 1u;
-          const uint32_t bits = static_cast<uint32_t>(path >> (8 * k)) & 0xFFu;
-          const int32_t row = (k0 + k) * C::BLK + C::ROWS * static_cast<int32_t>(pw) + static_cast<int32_t>(lane);
-          if (!warp_wait(empty(st), ((nb >> 1) & 1u) ^ 1u, 6)) { ok = false; break; }
-          copy_rows(st, table, lane < static_cast<uint32_t>(C::ROWS) && ((bits >> lane) & 1u) ? row : -1);
-          announce(st);
-        }
+        for (int32_t k = 0; k < n_tail && ok; ++k, ++nb)
+          ok = copy_block(table, (path >> k) & 1u ? (k0 + k) * C::BLK + block_row : -1);
       }
       if (!ok) break;
     }
-    // after an abort: the q copy in flight lands before the CTA may leave. Its phase is the last begun
-    if (tma_pending) attn_drain_wait(q_full, (n_q_loads - 1) & 1u, wt.aborted() ? kDrainBudgetNs : 0);
-  } else if (warp == C::MMA_WARP) {
-    // ================================================================ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc(1, 1, 0, 0, 128, C::BLK);
-      constexpr uint32_t idesc_o = make_idesc(1, 1, 0, 1, 128, C::OUT_DIMS);
-      const int32_t k_steps = (d_qk + 15) / 16;
-      uint32_t n_it = 0, n_busy = 0, nb = 0;
-      bool ok = true;
-      for (int32_t it = blockIdx.x; it < p.n_items && ok; it += gridDim.x, ++n_it) {
-        const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
-        if (!wt.wait(info_full(slot), sph, 10)) break;
-        const int32_t n_blocks = info_base[slot * C::INFO_WORDS] + info_base[slot * C::INFO_WORDS + 2];
-        mbar_arrive(info_empty(slot));
-        if (n_blocks == 0) continue;
-        const int32_t half = it % p.n_halves;
-        if (!wt.wait(q_full, n_busy & 1u, 11)) break;
-        // output of the item's block b - 1 after the logits of block b
-        for (int32_t b = 0; b <= n_blocks; ++b) {
-          if (b < n_blocks) {
-            // the stage's last user was block nb - 2; a full stage means its output MMAs, which read
-            // P from this logits buffer, are done
-            const uint32_t st = nb & 1u;
-            if (!wt.wait(full(st), (nb >> 1) & 1u, 12)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t tile = sbase + C::OFF_STAGE + st * C::STAGE_BYTES;
-            const uint32_t d = tmem + C::COL_S + C::BLK * st;
+    cp_async_wait<0>();
+    // after an abort the q copy in flight lands before the CTA may leave (else it has landed)
+    if (tma_pending && wt.aborted()) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
+  } else if (warp >= static_cast<uint32_t>(C::S_WARP)) {
+    // ================================================================ MMA issuers (even CTA), relay (odd CTA)
+    // One warp issues the logits MMAs, one the output MMAs, so that each one's waits (issue blocks
+    // while the pipe is full) overlap the other's work. A commit tracks the MMAs of its own thread.
+    constexpr uint32_t idesc_s = make_idesc(1, 1, 0, 0, 128, C::BLK);
+    constexpr uint32_t idesc_o = make_idesc(1, 1, 0, 1, 128, 256);
+    const bool logits = warp == static_cast<uint32_t>(C::S_WARP);
+    const int32_t out_instr = p.d_latent > 256 ? 2 : 1;
+    uint32_t n_it = 0, n_busy = 0, nb = 0;
+    bool ok = leader || logits;                          // the odd CTA's second warp has nothing to do
+    for (int32_t it = pair; it < p.n_items && ok; it += n_pairs, ++n_it) {
+      const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
+      if (!warp_wait(info_full(slot), sph, 10)) break;
+      const int32_t n_blocks = info_base[slot * C::INFO_WORDS] + info_base[slot * C::INFO_WORDS + 2];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(info_empty(slot));
+      if (n_blocks == 0) continue;
+      if (!leader) {
+        // relay: the odd CTA's softmax warps announce P locally (a CTA-scope arrive does not stall
+        // them); one cluster-scope arrive, which by cumulativity carries the observed P stores, follows
+        for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
+          if (!warp_wait(p_local(nb & 1u), (nb >> 1) & 1u, 11)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_cluster(p_full(nb & 1u) + lead_off);
+          __syncwarp();
+        }
+      } else if (logits) {
+        if (!warp_wait_pair(q_full, n_busy & 1u, 12)) break;
+        for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
+          const uint32_t st = nb & 1u, buf = nb % C::S_BUFS;
+          if (!warp_wait_pair(l_full(st), (nb >> 1) & 1u, 13)) { ok = false; break; }
+          if (!warp_wait(s_free(buf), ((nb / C::S_BUFS) & 1u) ^ 1u, 14)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d = tmem + C::COL_S + 32u * buf;
+          const uint64_t tile = sw128_desc(sbase + C::OFF_L + st * C::L_BYTES, 1, 1024);
+          const uint64_t qs = sw128_desc(sbase + C::OFF_QS, 1, 1024);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kDqk / 16; ++k) {
               if (k >= k_steps) break;
-              const uint64_t bd = sw128_desc(tile + (k >> 2) * C::ATOM + (k & 3) * 32, 1, 1024);
-              if (k < C::Q_TMEM_DIMS / 16) {
-                mma_bf16_ts(d, tmem + C::COL_Q + 8 * k, bd, idesc_s, k > 0 ? 1u : 0u);
+              const uint64_t bd = tile + static_cast<uint64_t>(((k >> 2) * C::L_ATOM + (k & 3) * 32) >> 4);
+              constexpr int kT = C::Q_TMEM_DIMS / 16;
+              if (k < kT) {
+                mma2_ts(d, tmem + C::COL_Q + 8 * k, bd, idesc_s, k > 0 ? 1u : 0u);
               } else {
-                const int kq = k - C::Q_TMEM_DIMS / 16;
-                mma_bf16_ss(d, sw128_desc(sbase + C::OFF_QS + (kq >> 2) * C::Q_ATOM + (kq & 3) * 32, 1, 1024), bd,
-                            idesc_s, 1u);
+                mma2_ss(d, qs + static_cast<uint64_t>((((k - kT) >> 2) * C::Q_ATOM + ((k - kT) & 3) * 32) >> 4), bd,
+                        idesc_s, 1u);
               }
             }
-            tc_commit(s_full(st));
-            if (b == n_blocks - 1) tc_commit(q_empty);
+            commit_pair(s_full(buf));
           }
-          if (b > 0) {
-            const uint32_t pn = nb - 1, st = pn & 1u;
-            if (!wt.wait(p_full(st), (pn >> 1) & 1u, 13)) { ok = false; break; }
-            if (b == 1 && !wt.wait(o_empty, (n_busy & 1u) ^ 1u, 14)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t tile = sbase + C::OFF_STAGE + st * C::STAGE_BYTES + half * (C::OUT_DIMS / 64) * C::ATOM;
-#pragma unroll
-            for (int k = 0; k < C::BLK / 16; ++k)
-              mma_bf16_ts(tmem + C::COL_O, tmem + C::COL_S + C::BLK * st + 8 * k,
-                          sw128_desc(tile + k * 2048, C::ATOM, 1024), idesc_o, (b > 1 || k > 0) ? 1u : 0u);
-            tc_commit(empty(st));
-          }
-          if (b < n_blocks) ++nb;
+          __syncwarp();
         }
         if (!ok) break;
-        tc_commit(o_full);
-        ++n_busy;
+        if (elect_one()) commit_pair(q_empty);
+      } else {
+        if (!warp_wait_pair(o_empty, (n_busy & 1u) ^ 1u, 15)) break;
+        for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
+          const uint32_t st = nb & 1u;
+          if (!warp_wait_pair(v_full(st), (nb >> 1) & 1u, 16)) { ok = false; break; }
+          if (!warp_wait_pair(p_full(st), (nb >> 1) & 1u, 17)) { ok = false; break; }
+          if (lane == 0) mbar_arrive(s_free(nb % C::S_BUFS));    // the softmax is done with that logits buffer
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t pd = sw128_desc(sbase + C::OFF_P + st * C::P_BYTES, 1, 1024);
+          const uint64_t tile = sw128_desc(sbase + C::OFF_O + st * C::O_BYTES, C::O_ATOM, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (i >= out_instr) break;
+#pragma unroll
+              for (int k = 0; k < C::BLK / 16; ++k)
+                mma2_ss(tmem + C::COL_O + 128 * i, pd + static_cast<uint64_t>((32 * k) >> 4),
+                        tile + static_cast<uint64_t>((2 * i * C::O_ATOM + 2048 * k) >> 4), idesc_o,
+                        (b > 0 || k > 0) ? 1u : 0u);
+            }
+            commit_pair(o_done(st));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) commit_pair(o_full);
       }
-      tc_commit(mma_done);
+      ++n_busy;
+    }
+    if (leader && elect_one()) {
+      commit2(mma_done);
       attn_drain_wait(mma_done, 0, kDrainBudgetNs);
     }
   } else {
-    // ================================================================ softmax (thread = head = TMEM lane)
-    const int32_t head = static_cast<int32_t>(threadIdx.x);
+    // ================================================================ softmax (TMEM lane = thread)
+    // Lane L: head 64 rank + L % 64; logits of block rows 32 (L / 64) ..; output dims 256 i + 128 (L / 64) ..
+    // Warps w and w + 2 hold the halves of the same 32 heads' rows and exchange their maxima.
+    const uint32_t L = threadIdx.x, part = L >> 6, hl = L & 63u;
+    const int32_t head = static_cast<int32_t>(64u * rank + hl);
     const uint32_t lane_off = (warp * 32u) << 16;
     const float sc = p.scale_log2;
-    uint32_t n_it = 0, n_busy = 0, nb = 0;
-    for (int32_t it = blockIdx.x; it < p.n_items; it += gridDim.x, ++n_it) {
+    uint32_t n_it = 0, n_busy = 0, nb = 0, nx = 0;
+    bool ok = true;
+    // One float from the thread with the other half of the row. Each thread has two words and stores
+    // (number, value) in one; a word is used again only after the partner has answered the next
+    // exchange, so no unread value is overwritten.
+    const uint32_t xchg = sbase + C::OFF_XCHG;
+    auto swap_partner = [&](float mine) -> float {
+      const uint32_t at = xchg + (nx & 1u) * (128u * 8u);
+      ++nx;
+      const uint64_t word = (static_cast<uint64_t>(nx) << 32) | __float_as_uint(mine);
+      asm volatile("st.volatile.shared.u64 [%0], %1;" ::"r"(at + L * 8u), "l"(word) : "memory");
+      uint32_t v = 0;
+      const bool got = wt.wait_word(at + (L ^ 64u) * 8u, nx, 24, v);
+      if (!__all_sync(0xffffffffu, got)) ok = false;
+      return __uint_as_float(v);
+    };
+    for (int32_t it = pair; it < p.n_items && ok; it += n_pairs, ++n_it) {
       const Item m = item_of(it);
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
       if (!warp_wait(info_full(slot), sph, 20)) break;
       volatile int32_t* info = info_base + slot * C::INFO_WORDS;
       const int32_t n_list = info[0], end = info[1], n_tail = info[2], k0 = info[3];
-      uint32_t path[kTree ? kMaxDraft / 32 : 1];
+      uint32_t path[kTree ? kMaxDraft / 64 : 1];         // this half's words of the drafted blocks
       if constexpr (kTree) {
 #pragma unroll
-        for (int w = 0; w < kMaxDraft / 32; ++w) path[w] = static_cast<uint32_t>(info[4 + w]);
+        for (int w = 0; w < kMaxDraft / 64; ++w) path[w] = static_cast<uint32_t>(info[4 + 2 * w + part]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(info_empty(slot));
       const int32_t n_blocks = n_list + n_tail;
-      const int32_t dim0 = C::OUT_DIMS * m.half, dims = min(C::OUT_DIMS, p.d_latent - dim0);
       const size_t row = static_cast<size_t>(m.qi) * p.n_heads + head;                       // (query, head)
       const size_t prow = (static_cast<size_t>(m.qi) * p.n_splits + m.split) * p.n_heads + head;
       const bool writes = head < p.n_heads;
       if (n_blocks == 0) {
         if (writes) {
           if (p.n_splits == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.d_latent + dim0);
-            for (int32_t c = 0; c < dims / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-            if (m.half == 0) p.lse[row] = -INFINITY;
-          } else if (m.half == 0) {
+            for (int32_t d = 128 * static_cast<int32_t>(part); d < p.d_latent; d += 256)
+              for (int32_t u = d; u < min(d + 128, p.d_latent); u += 8)
+                *reinterpret_cast<uint4*>(p.out + row * p.d_latent + u) = make_uint4(0, 0, 0, 0);
+            if (part == 0) p.lse[row] = -INFINITY;
+          } else if (part == 0) {
             p.part_lse[prow] = -INFINITY;
           }
         }
         continue;
       }
-      // entry `lane` / 32 + lane of list block b, read one block ahead: a ballot gives the valid rows
+      // entry 32 part + lane of list block b, read one block ahead: a ballot gives the valid rows
       const int32_t* idx_row = p.idx + static_cast<size_t>(m.qi) * p.topk;
-      auto entry = [&](int32_t b, int32_t h) -> int32_t {
-        const int32_t j = m.e0 + b * C::BLK + 32 * h + static_cast<int32_t>(lane);
+      auto entry = [&](int32_t b) -> int32_t {
+        const int32_t j = m.e0 + b * C::BLK + static_cast<int32_t>(32u * part + lane);
         return b < n_list && j < end ? __ldg(idx_row + j) : -1;
       };
-      int32_t v0 = entry(0, 0), v1 = entry(0, 1);
+      int32_t v = entry(0);
       float m2 = -INFINITY, l_r = 0.f, l_f = 0.f;        // running max; sums of rounded and unrounded weights
-      bool ok = true;
       for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
-        const uint32_t st = nb & 1u;
-        uint32_t vm0 = __ballot_sync(0xffffffffu, v0 >= 0 && v0 < p.max_len);
-        uint32_t vm1 = __ballot_sync(0xffffffffu, v1 >= 0 && v1 < p.max_len);
+        const uint32_t buf = nb % C::S_BUFS, st = nb & 1u;
+        uint32_t vm = __ballot_sync(0xffffffffu, v >= 0 && v < p.max_len);
         if constexpr (kTree) {
           if (b >= n_list) {
-            const int32_t k = 2 * (k0 + b - n_list);
+            const int32_t k = k0 + b - n_list;
 #pragma unroll
-            for (int w = 0; w < kMaxDraft / 32; w += 2)
-              if (w == k) { vm0 = path[w]; vm1 = path[w + 1]; }
+            for (int w = 0; w < kMaxDraft / 64; ++w)
+              if (w == k) vm = path[w];
           }
         }
-        v0 = entry(b + 1, 0);
-        v1 = entry(b + 1, 1);
-        if (!warp_wait(s_full(st), (nb >> 1) & 1u, 21)) { ok = false; break; }
+        v = entry(b + 1);
+        if (!warp_wait(s_full(buf), (nb / C::S_BUFS) & 1u, 21)) { ok = false; break; }
         tc_fence_after();
-        uint32_t z[C::BLK];
-        tmem_ld32(tmem + lane_off + C::COL_S + C::BLK * st, *reinterpret_cast<uint32_t(*)[32]>(&z[0]));
-        tmem_ld32(tmem + lane_off + C::COL_S + C::BLK * st + 32, *reinterpret_cast<uint32_t(*)[32]>(&z[32]));
+        uint32_t z[32];
+        tmem_ld32(tmem + lane_off + C::COL_S + 32u * buf, z);
         tmem_wait_ld();
-        if ((vm0 & vm1) != 0xffffffffu) {
+        tc_fence_before();
+        if (vm != 0xffffffffu) {
 #pragma unroll
-          for (int j = 0; j < C::BLK; ++j)
-            if (!(((j < 32 ? vm0 : vm1) >> (j & 31)) & 1u)) z[j] = __float_as_uint(-INFINITY);
+          for (int j = 0; j < 32; ++j)
+            if (!((vm >> j) & 1u)) z[j] = __float_as_uint(-INFINITY);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < C::BLK; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(z[j]));
-        const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;     // sc > 0
+        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(z[j]));
+        float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;     // sc > 0
+        mb = fmaxf(mb, swap_partner(mb));
+        if (!ok) break;
         const bool need = mb > m2 + kLazyRescale;
         float alpha = 1.0f;
         if (need) {
@@ -573,10 +754,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         }
         // while every row seen so far was masked m2 is -inf: subtract 0, so that P = 2^-inf = 0
         const float msub = m2 == -INFINITY ? 0.0f : m2;
-        uint32_t pk[C::BLK / 2];
+        uint32_t pk[16];
         float fr[2] = {0.f, 0.f}, ff[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < C::BLK / 2; ++j) {
+        for (int j = 0; j < 16; ++j) {
           const float a0 = ex2_approx(fmaf(__uint_as_float(z[2 * j]), sc, -msub));
           const float a1 = ex2_approx(fmaf(__uint_as_float(z[2 * j + 1]), sc, -msub));
           const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);
@@ -589,68 +770,77 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         }
         l_r += fr[0] + fr[1];
         l_f += ff[0] + ff[1];
-        // ---- the output so far follows the raised max once the previous block's MMAs are in it
+        // ---- the P buffer is free once the outputs of block nb - 2 are done; a raised max waits for those
+        // of block nb - 1, and rescales this lane's outputs
         if (b > 0 && __any_sync(0xffffffffu, need)) {
-          if (!warp_wait(empty(st ^ 1u), ((nb - 1) >> 1) & 1u, 22)) { ok = false; break; }
+          if (!warp_wait(o_done(st ^ 1u), ((nb - 1) >> 1) & 1u, 22)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < C::OUT_DIMS / 16; ++c) {
+          for (int k = 0; k < 16; ++k) {
             uint32_t o[16];
-            tmem_ld16(tmem + lane_off + C::COL_O + 16 * c, o);
+            tmem_ld16(tmem + lane_off + C::COL_O + 16 * k, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int v = 0; v < 16; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * alpha);
-            tmem_st16(tmem + lane_off + C::COL_O + 16 * c, o);
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+            tmem_st16(tmem + lane_off + C::COL_O + 16 * k, o);
           }
+          tmem_wait_st();
+          tc_fence_before();
+        } else if (nb >= 2) {
+          if (!warp_wait(o_done(st), ((nb >> 1) & 1u) ^ 1u, 23)) { ok = false; break; }
         }
-        // ---- P over the logits: column j holds rows 2j and 2j+1
-        tmem_st16(tmem + lane_off + C::COL_S + C::BLK * st, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
-        tmem_st16(tmem + lane_off + C::COL_S + C::BLK * st + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
-        tmem_wait_st();
-        tc_fence_before();
+        // ---- P row hl, columns 32 part .. +31: four chunks of the 128-byte swizzled row
+        const uint32_t prow_at = sbase + C::OFF_P + st * C::P_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          st_shared_v4(prow_at + sw128_offset(hl, 4 * part + k), make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(st));
+        if (lane == 0) mbar_arrive(leader ? p_full(st) : p_local(st));
       }
       if (!ok) break;
       // ---- normalise and store. A sum of zero (no row attended) gives zeros and -inf.
-      if (!warp_wait(o_full, n_busy & 1u, 23)) break;
+      l_r += swap_partner(l_r);
+      l_f += swap_partner(l_f);
+      if (!ok || !warp_wait(o_full, n_busy & 1u, 25)) break;
       ++n_busy;
       tc_fence_after();
       const float inv = l_r == 0.f ? 0.f : 1.0f / l_r;
 #pragma unroll 1
-      for (int c = 0; c < C::OUT_DIMS / 32; ++c) {
+      for (int k = 0; k < 8; ++k) {                      // 2 instructions x 128 columns, 32 at a time
+        const int32_t dim = 256 * (k >> 2) + 128 * static_cast<int32_t>(part) + 32 * (k & 3);
         uint32_t o[32];
-        tmem_ld32(tmem + lane_off + C::COL_O + 32 * c, o);
+        tmem_ld32(tmem + lane_off + C::COL_O + 32 * k, o);
         tmem_wait_ld();
         if (!writes) continue;
         if (p.n_splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.d_latent + dim0 + 32 * c);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.d_latent + dim);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            if (32 * c + 8 * v >= dims) break;
+          for (int u = 0; u < 4; ++u) {
+            if (dim + 8 * u >= p.d_latent) break;
             uint32_t w[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(o[8 * v + 2 * u]) * inv,
-                                                              __uint_as_float(o[8 * v + 2 * u + 1]) * inv);
-              w[u] = *reinterpret_cast<const uint32_t*>(&pr);
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * x]) * inv,
+                                                              __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+              w[x] = *reinterpret_cast<const uint32_t*>(&pr);
             }
-            dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_out + prow * p.d_latent + dim0 + 32 * c);
+          float4* dst = reinterpret_cast<float4*>(p.part_out + prow * p.d_latent + dim);
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            if (32 * c + 4 * v >= dims) break;
-            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                 __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+          for (int u = 0; u < 8; ++u) {
+            if (dim + 4 * u >= p.d_latent) break;
+            dst[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                                 __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty);
-      if (writes && m.half == 0) {
+      if (lane == 0) arrive_leader(o_empty);
+      if (writes && part == 0) {
         const float l2 = l_f == 0.f ? -INFINITY : m2 + log2f(l_f);
         if (p.n_splits == 1) p.lse[row] = l2 * 0.69314718055994531f;
         else p.part_lse[prow] = l2;
@@ -660,10 +850,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   // ---- teardown: every role reaches here (all waits are bounded)
   tc_fence_before();
   __syncthreads();
-  if (warp == C::MMA_WARP) {
+  cluster_sync();            // no CTA leaves while its peer may still use its memory
+  if (warp == C::S_WARP) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
   }
 }
 

@@ -216,12 +216,13 @@ DeviceInfo device_info() {
     cudaFuncSetAttribute(sparse_mla_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          AttnCfg::SMEM_BYTES);
     cudaFuncSetAttribute(indexer_kl_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, KlCfg::SMEM_BYTES);
-    cudaFuncSetAttribute(cache_attn_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         CacheAttnCfg::SMEM_BYTES);
-    cudaFuncSetAttribute(cache_attn_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         CacheAttnCfg::SMEM_BYTES);
-    cudaFuncSetAttribute(cache_attn_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         CacheAttnCfg::SMEM_BYTES);
+    for (const void* f : {reinterpret_cast<const void*>(cache_attn_kernel<true, false>),
+                          reinterpret_cast<const void*>(cache_attn_kernel<true, true>),
+                          reinterpret_cast<const void*>(cache_attn_kernel<false, true>)}) {
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, CacheAttnCfg::SMEM_BYTES);
+      // the smallest carveout that holds it (196 of 228 KB): the rest is L1
+      cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, 84);
+    }
     cudaFuncAttributes fa{};
     cache[dev].indexer_regs_ok = cudaFuncGetAttributes(&fa, indexer_topk_kernel<kPrefillNQ>) == cudaSuccess &&
                                  fa.numRegs == IdxCfg<kPrefillNQ>::LAUNCH_REGS;
@@ -273,14 +274,14 @@ bool encode_q_bf16(CUtensorMap* map, const void* base, uint64_t rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Queries of any supported dims as a 2-D bf16 tensor [rows = B*n_q*n_heads, d], box {64 dims, 128 rows}.
+// Queries of any supported dims as a 2-D bf16 tensor [rows = B*n_q*n_heads, d], box {64 dims, 64 rows}.
 // Rows and dims past the tensor's end are filled with zeros.
 bool encode_q_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t d) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {d, rows, 1};
   const cuuint64_t strides[2] = {d * 2, rows * d * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kHeads), 1};
+  const cuuint32_t box[3] = {64, 64, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -830,15 +831,15 @@ int row_grid(int64_t rows, int sms) {
 }
 
 // How the rows of a query are split (see cache_attn.cuh). The cost of a split is what the slowest
-// SM does: its items one after another, each a fixed part (q, statistics, output) and its blocks,
+// pair of SMs does: its items one after another, each a fixed part (q, statistics, output) and its blocks,
 // and, with more than one range, the join: a launch, and the ranges' outputs written and read.
 struct CachePlan {
-  int32_t n_halves, n_splits, split_blocks;
+  int32_t n_splits, split_blocks;
 };
-constexpr int64_t kPlanSms = 148;
+constexpr int64_t kPlanPairs = 74;
 constexpr int64_t kPlanItemNs = 2500, kPlanBlockNs = 1200, kPlanJoinNs = 3000, kPlanPartNs = 130;
 CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
-  CachePlan best{d.d_latent > CacheAttnCfg::OUT_DIMS ? 2 : 1, 1, 1};
+  CachePlan best{1, 1};
   const int64_t queries = static_cast<int64_t>(d.batch) * d.n_q;
   const int32_t blocks = (topk + CacheAttnCfg::BLK - 1) / CacheAttnCfg::BLK +
                          (tree ? (d.n_q + CacheAttnCfg::BLK - 1) / CacheAttnCfg::BLK : 0);
@@ -847,8 +848,7 @@ CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
   for (int32_t per = blocks; per >= 1; --per) {
     const int32_t splits = (blocks + per - 1) / per;
     if (least >= 0 && splits == best.n_splits) continue;
-    const int64_t items = queries * splits * best.n_halves;
-    const int64_t waves = (items + kPlanSms - 1) / kPlanSms;
+    const int64_t waves = (queries * splits + kPlanPairs - 1) / kPlanPairs;
     int64_t cost = waves * (kPlanItemNs + per * kPlanBlockNs);
     if (splits > 1) cost += kPlanJoinNs + kPlanPartNs * queries * splits;
     if (least < 0 || cost < least) {
@@ -878,7 +878,7 @@ CacheLayout cache_layout(const dsa_dims& d, const CachePlan& plan) {
 
 template <bool kQuant, bool kTree>
 dsa_status launch_cache_attn(const CUtensorMap& map_q, const CacheAttnParams& p, int sms, cudaStream_t st) {
-  const int grid = static_cast<int>(std::min<int64_t>(p.n_items, sms));
+  const int grid = 2 * static_cast<int>(std::max(1, std::min(p.n_items, sms / 2)));
   cache_attn_kernel<kQuant, kTree><<<grid, CacheAttnCfg::THREADS, CacheAttnCfg::SMEM_BYTES, st>>>(map_q, p);
   return from_cuda(cudaGetLastError());
 }
@@ -897,7 +897,7 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   const CacheLayout L = cache_layout(d, plan);
   if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
   if (queries == 0) return DSA_OK;
-  if (queries * d.n_heads >= (int64_t(1) << 31) || queries * plan.n_splits * plan.n_halves >= (int64_t(1) << 31))
+  if (queries * d.n_heads >= (int64_t(1) << 31) || queries * plan.n_splits >= (int64_t(1) << 31))
     return DSA_ERR_UNSUPPORTED;
   if (!q || !idx || !out || !lse || (cache == nullptr && !kv) || (tree && (!draft || !parents)))
     return DSA_ERR_INVALID_ARG;
@@ -927,10 +927,9 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   p.n_heads = d.n_heads;
   p.d_latent = d.d_latent;
   p.d_rope = d.d_rope;
-  p.n_halves = plan.n_halves;
   p.n_splits = plan.n_splits;
   p.split_blocks = plan.split_blocks;
-  p.n_items = static_cast<int32_t>(queries * plan.n_splits * plan.n_halves);
+  p.n_items = static_cast<int32_t>(queries * plan.n_splits);
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
   p.wait_budget_ns = kWaitBudgetNs;
   CUtensorMap map_q;
