@@ -202,8 +202,8 @@ dsa_status dsa_indexer_topk_decode_noalloc(const dsa_dims* dims, const void* q_i
  *   scale = 2^e, e the smallest integer with amax <= 448 * 2^e, held to -100..100 (1 if amax is 0)
  *   code  = E4M3(x / scale), round to nearest even
  * Infinities, and magnitudes above 448 * 2^100, become the largest code; a group that holds a NaN
- * gets the scale NaN and reads as NaN throughout. code * scale is exact in bf16. A cache filled by
- * other means must hold scales of that form (powers of two, or NaN) and no NaN codes (0x7F, 0xFF).
+ * gets the scale NaN and reads as NaN throughout. code * scale is exact in bf16. In a cache filled by
+ * other means a scale may be any fp32: a value is then code * scale rounded to fp32 and to bf16.
  * The calls on an 8-bit cache require d_latent % 16 == 0 (else DSA_ERR_UNSUPPORTED).
  */
 typedef struct {

@@ -307,14 +307,13 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     const uint32_t gt = (pw % C::PART_WARPS) * 32u + lane;   // thread of the part, 0..255
     // Logits part: eight threads per row, thread c has the row's 16-dim pieces c, c + 8, ...: one per
     // scale group. Output part: four threads per row, thread c has piece c of each of the four atoms.
-    // A store instruction of eight threads then covers eight 16-byte chunks in distinct bank groups
-    // (logits part: two atoms, so the threads of the second store their two chunks in opposite order).
-    const uint32_t row = logits_part ? gt >> 3 : gt >> 2;    // row of the part's tile
-    const uint32_t c = logits_part ? gt & 7u : gt & 3u;
+    // Eight threads in a row hold four pieces of one atom in two neighbouring rows, so that the eight
+    // 16-byte chunks which they store at once fall into distinct bank groups of the swizzled tile.
+    const uint32_t row = logits_part ? 4u * (gt >> 5) + 2u * (lane >> 4) + ((lane >> 2) & 1u) : gt >> 2;   // of the tile
+    const uint32_t c = logits_part ? (lane & 3u) + 4u * ((lane >> 3) & 1u) : lane & 3u;
     const uint32_t row_at = (row >> 3) * 1024u + (row & 7u) * 128u;
     const uint32_t at0 = row_at + (((2 * (c & 3u)) ^ (row & 7u)) << 4);
     const uint32_t at1 = row_at + (((2 * (c & 3u) + 1) ^ (row & 7u)) << 4);
-    const bool swap = logits_part && (c & 4u) != 0;
     const int32_t block_row = static_cast<int32_t>(row + (logits_part ? 32u * rank : 0u));   // row of the block
     // piece k of this thread: its first dim, and where it goes in the tile
     auto piece_dim = [&](int32_t k) -> int32_t {
@@ -531,10 +530,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
           for (int k = 0; k < 4; ++k) {
             if (piece_dim(k) >= p.d_latent) break;
             uint4 lo, hi;
-            const Dequant expand(sc[k]);
-            expand(raw[k], lo, hi);
-            st_shared_v4(tile + piece_at(k) + (swap ? at1 : at0), swap ? hi : lo);
-            st_shared_v4(tile + piece_at(k) + (swap ? at0 : at1), swap ? lo : hi);
+            expand16(raw[k], sc[k], lo, hi);
+            st_shared_v4(tile + piece_at(k) + at0, lo);
+            st_shared_v4(tile + piece_at(k) + at1, hi);
           }
           if (has_rope) {
             st_shared_v4(tile + piece_at(rope_k) + at0, rp[0]);
@@ -755,21 +753,27 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         // while every row seen so far was masked m2 is -inf: subtract 0, so that P = 2^-inf = 0
         const float msub = m2 == -INFINITY ? 0.0f : m2;
         uint32_t pk[16];
-        float fr[2] = {0.f, 0.f}, ff[2] = {0.f, 0.f};
+        uint64_t sum_r = 0, sum_f = 0;                   // packed pairs of fp32
+        const uint64_t sc2 = pack_f32x2(sc, sc), msub2 = pack_f32x2(-msub, -msub);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const float a0 = ex2_approx(fmaf(__uint_as_float(z[2 * j]), sc, -msub));
-          const float a1 = ex2_approx(fmaf(__uint_as_float(z[2 * j + 1]), sc, -msub));
+          uint64_t x = pack_f32x2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1]));
+          asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(sc2), "l"(msub2));
+          float a0, a1;
+          unpack_f32x2(x, a0, a1);
+          a0 = ex2_approx(a0);
+          a1 = ex2_approx(a1);
           const __nv_bfloat162 pr = __floats2bfloat162_rn(a0, a1);
           const float2 back = __bfloat1622float2(pr);
-          fr[0] += back.x;
-          fr[1] += back.y;
-          ff[0] += a0;
-          ff[1] += a1;
+          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum_r) : "l"(pack_f32x2(back.x, back.y)));
+          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum_f) : "l"(pack_f32x2(a0, a1)));
           pk[j] = *reinterpret_cast<const uint32_t*>(&pr);
         }
-        l_r += fr[0] + fr[1];
-        l_f += ff[0] + ff[1];
+        float s0, s1;
+        unpack_f32x2(sum_r, s0, s1);
+        l_r += s0 + s1;
+        unpack_f32x2(sum_f, s0, s1);
+        l_f += s0 + s1;
         // ---- the P buffer is free once the outputs of block nb - 2 are done; a raised max waits for those
         // of block nb - 1, and rescales this lane's outputs
         if (b > 0 && __any_sync(0xffffffffu, need)) {
