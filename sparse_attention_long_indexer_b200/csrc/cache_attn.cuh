@@ -70,9 +70,9 @@ struct CacheAttnCfg {
   static constexpr int OFF_P = OFF_QS + QS_ATOMS * Q_ATOM;         // 2 buffers
   static constexpr int OFF_XCHG = OFF_P + 2 * P_BYTES;             // [2][128] tagged words
   static constexpr int OFF_INFO = OFF_XCHG + 2 * 128 * 8;
-  static constexpr int INFO_WORDS = 4 + kMaxDraft / 32;  // list blocks, list end, tail blocks, first tail block, path
+  static constexpr int INFO_WORDS = 4 + kMaxDraft / 32;  // list blocks, drafted blocks, first drafted block, -, path
   static constexpr int OFF_BAR = OFF_INFO + 2 * INFO_WORDS * 4;
-  static constexpr int NUM_BARS = 26;
+  static constexpr int NUM_BARS = 28;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static_assert(OFF_O % 1024 == 0 && OFF_QS % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "layout");
@@ -114,6 +114,16 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t dst, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -204,17 +214,20 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   auto o_done = [&](uint32_t j) { return B(7 + j); };        // commit (2): outputs of a block done, its part and P read
   const uint32_t o_full = B(9);                              // commit: the item's outputs are done
   const uint32_t q_empty = B(10);                            // commit: the item's logits are done
-  const uint32_t q_tma = B(11);                              // this CTA's part of q in shared memory has landed
+  const uint32_t q_tma = B(11);                              // this CTA's q has landed in shared memory
   auto p_local = [&](uint32_t j) { return B(12 + j); };      // odd CTA's softmax warps: P written
   // in the even CTA, arrived on by both
   auto l_full = [&](uint32_t s) { return B(14 + s); };       // producer warps: a logits part is in
   auto v_full = [&](uint32_t s) { return B(16 + s); };       // producer warps: an output part is in
-  const uint32_t q_full = B(18);                             // producer warps and the TMA part
+  const uint32_t q_full = B(18);                             // producer warps: q is in (TMEM and shared memory)
   auto p_full = [&](uint32_t j) { return B(19 + j); };       // its softmax warps, and the odd CTA's relay
   const uint32_t o_empty = B(21);                            // softmax warps: outputs read
   // in the even CTA only: a logits buffer is free, once the output warp has seen its block's P
   auto s_free = [&](uint32_t i) { return B(22 + i); };       // (3)
   const uint32_t mma_done = B(25);
+  // in both CTAs
+  const uint32_t q_read = B(26);                             // producer warps: q is out of the logits ring
+  const uint32_t stored = B(27);                             // softmax warps: an item's outputs are out of the P buffers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
@@ -239,11 +252,14 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     mbar_init(o_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(q_tma, 1);
-    mbar_init(q_full, 2 * (C::PART_WARPS + 1));
+    mbar_init(q_full, 2 * C::PRODUCER_WARPS);
+    mbar_init(q_read, C::PRODUCER_WARPS);
+    mbar_init(stored, C::SOFTMAX_WARPS);
     mbar_init(o_empty, 2 * C::SOFTMAX_WARPS);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
+    prefetch_tensormap(&map_q);
   }
   // exchange numbers start at 1
   for (uint32_t i = threadIdx.x; i < 256u; i += C::THREADS) reinterpret_cast<uint64_t*>(smem + C::OFF_XCHG)[i] = 0;
@@ -267,15 +283,21 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     if (leader) mbar_arrive(bar);
     else mbar_arrive_cluster(bar + lead_off);
   };
+  // Lane 0 waits for the warp. The warp barrier orders the other lanes' accesses behind its acquire (the
+  // shuffle alone does not: their loads may be moved above it).
   auto warp_wait = [&](uint32_t bar, uint32_t parity, uint32_t tag) -> bool {
     uint32_t got = 1;
     if (lane == 0) got = wt.wait(bar, parity, tag) ? 1u : 0u;
-    return __shfl_sync(0xffffffffu, got, 0) != 0;
+    got = __shfl_sync(0xffffffffu, got, 0);
+    __syncwarp();
+    return got != 0;
   };
   auto warp_wait_pair = [&](uint32_t bar, uint32_t parity, uint32_t tag) -> bool {
     uint32_t got = 1;
     if (lane == 0) got = wt.template wait<true>(bar, parity, tag) ? 1u : 0u;
-    return __shfl_sync(0xffffffffu, got, 0) != 0;
+    got = __shfl_sync(0xffffffffu, got, 0);
+    __syncwarp();
+    return got != 0;
   };
 
   // item -> (query, range of its rows)
@@ -332,6 +354,18 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       const int32_t node = m.qi % p.n_q;
       const int64_t seq = m.qi / p.n_q;
       const int32_t* idx_row = p.idx + static_cast<size_t>(m.qi) * p.topk;
+      // this thread's entry of list block b (read ahead of its use), and the row it stands for, or -1.
+      // Entries from the extent of the range on are padding, so they need no extra check.
+      auto entry = [&](int32_t b) -> int32_t {
+        const int32_t j = m.e0 + b * C::BLK + block_row;
+        return j < m.e1 ? __ldg(idx_row + j) : -1;
+      };
+      auto checked = [&](int32_t v) -> int32_t {
+        if (v < p.max_len) return v;
+        record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(m.qi));
+        return -1;
+      };
+      const int32_t v0 = entry(0), v1 = entry(1);
       if (pw == 0) {
         // ---- the extent of the list in this range (one past its last entry >= 0, found from the
         // end), and the node's path through the tree
@@ -382,16 +416,15 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         }
         if (lane == 0) {
           info[0] = n_list;
-          info[1] = end;
-          info[2] = n_tail;
-          info[3] = m.k0;
+          info[1] = n_tail;
+          info[2] = m.k0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(info_full(slot));
       } else {
         if (!warp_wait(info_full(slot), sph, 2)) break;
       }
-      const int32_t n_list = info[0], end = info[1], n_tail = info[2], k0 = info[3];
+      const int32_t n_list = info[0], n_tail = info[1], k0 = info[2];
       uint32_t path = 0;                                 // bit k: this thread's row of drafted block k0 + k is attended
       if constexpr (kTree) {
         for (int32_t k = 0; k < n_tail; ++k)
@@ -401,49 +434,62 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       if (pw != 0 && lane == 0) mbar_arrive(info_empty(slot));
       if (n_list + n_tail == 0) continue;
 
-      if (logits_part) {
-        // ---- q: dims 0..319 into this warp's TMEM lanes (both lane halves hold this CTA's 64 heads), the
-        // rest by TMA, once the previous item's logits MMAs have read theirs. Heads and dims past the
-        // query's own are zeros in TMEM; the TMA part past the last dim is zero-filled, and rows past
-        // the last head only reach unused lanes.
-        if (!warp_wait(q_empty, (n_busy & 1u) ^ 1u, 3)) break;
-        const int32_t atoms = (d_qk - C::Q_TMEM_DIMS + 63) / 64;
-        if (pw == 0 && lane == 0 && atoms > 0) {
+      // ---- q, once the previous item's logits MMAs have read theirs: all dims by TMA, dims 320.. where
+      // they stay, dims 0..319 into the logits ring, which is free then, and from there into the
+      // TMEM lanes (both lane halves hold this CTA's 64 heads; every producer warp a lane quarter and
+      // 80 dims). A load per lane straight from global memory touches a line each and took 5K clocks.
+      // Past the query's last dim TMA fills zeros; rows past its last head only reach unused lanes.
+      const uint32_t q_par = n_busy & 1u;
+      ++n_busy;
+      if (pw == 0) {
+        if (!warp_wait(q_empty, q_par ^ 1u, 3)) break;
+        if (lane == 0) {
+          const int32_t atoms = (d_qk + 63) / 64;
+          fence_proxy_async_smem();                        // the ring's earlier stores before TMA's
           mbar_expect_tx(q_tma, static_cast<uint32_t>(atoms) * C::Q_ATOM);
           tma_pending = true;
-          for (int32_t a = 0; a < atoms; ++a)
-            tma_load_3d(sbase + C::OFF_QS + a * C::Q_ATOM, &map_q, q_tma, C::Q_TMEM_DIMS + 64 * a,
-                        m.qi * p.n_heads + 64 * static_cast<int32_t>(rank), 0);
+          for (int32_t t = 0; t < atoms; ++t)
+            tma_load_3d(sbase + (t < C::Q_TMEM_DIMS / 64 ? C::OFF_L + t * C::Q_ATOM
+                                                         : C::OFF_QS + (t - C::Q_TMEM_DIMS / 64) * C::Q_ATOM),
+                        &map_q, q_tma, 64 * t, m.qi * p.n_heads + 64 * static_cast<int32_t>(rank), 0);
         }
+        __syncwarp();
+      }
+      auto bring_q = [&]() -> bool {
+        if (!warp_wait(q_tma, q_par, 4)) return false;
         tc_fence_after();
-        const int32_t head = static_cast<int32_t>(64u * rank + ((32u * (warp & 3u) + lane) & 63u));
-        const int32_t dim0 = C::Q_TMEM_DIMS / 2 * static_cast<int32_t>(pw >> 2);
-        const __nv_bfloat16* qrow = p.q + (static_cast<size_t>(m.qi) * p.n_heads + head) * d_qk + dim0;
-#pragma unroll 1
-        for (int k = 0; k < C::Q_TMEM_DIMS / 2 / 32; ++k) {      // 16 columns (32 dims) at a time
-          uint32_t r[16];
+        constexpr uint32_t kChunks = C::Q_TMEM_DIMS / 8 / (C::PRODUCER_WARPS / 4);   // 10 of 16 bytes
+        static_assert(kChunks == 10 && 5 * C::Q_ATOM <= 2 * C::L_BYTES, "column stores, staging");
+        const uint32_t hl = (32u * (warp & 3u) + lane) & 63u;
+        const uint32_t at = tmem + ((32u * (warp & 3u)) << 16) + C::COL_Q + 4 * kChunks * (pw >> 2);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const bool in = head < p.n_heads && dim0 + 32 * k + 8 * v < d_qk;
-            const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(qrow) + 4 * k + v) : make_uint4(0, 0, 0, 0);
+        for (uint32_t v0 = 0; v0 < kChunks; v0 += 2) {
+          uint32_t r[8];
+#pragma unroll
+          for (uint32_t v = 0; v < 2; ++v) {
+            const uint32_t ch = kChunks * (pw >> 2) + v0 + v;
+            // past the last atom that was loaded the ring holds whatever it held
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (static_cast<int32_t>(8 * ch) < d_qk)
+              u = ld_shared_v4(sbase + C::OFF_L + (ch >> 3) * C::Q_ATOM + sw128_offset(hl, ch & 7u));
             r[4 * v + 0] = u.x;
             r[4 * v + 1] = u.y;
             r[4 * v + 2] = u.z;
             r[4 * v + 3] = u.w;
           }
-          tmem_st16(tmem + ((32u * (warp & 3u)) << 16) + C::COL_Q + dim0 / 2 + 16 * k, r);
+          tmem_st8(at + 4 * v0, r);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           arrive_leader(q_full);
-          if (pw == 0 && (atoms <= 0 || wt.wait(q_tma, n_busy & 1u, 4))) arrive_leader(q_full);
+          mbar_arrive(q_read);
         }
         __syncwarp();
-      }
-      ++n_busy;
-
+        // the ring may be filled once every warp has read its part
+        return !logits_part || warp_wait(q_read, q_par, 7);
+      };
       // ---- the blocks
       // waits for the part's stage of block nb, and gives it
       auto acquire = [&](uint32_t& tile) -> bool {
@@ -459,16 +505,6 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_leader(logits_part ? l_full(nb & 1u) : v_full(nb & 1u));
-      };
-      // this thread's entry of list block b (read ahead of its use), and the row it stands for, or -1
-      auto entry = [&](int32_t b) -> int32_t {
-        const int32_t j = m.e0 + b * C::BLK + block_row;
-        return b < n_list && j < end ? __ldg(idx_row + j) : -1;
-      };
-      auto checked = [&](int32_t v) -> int32_t {
-        if (v < p.max_len) return v;
-        record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(m.qi));
-        return -1;
       };
       // one block of bf16 rows: row r of a table, zeros where r < 0
       auto copy_block = [&](const __nv_bfloat16* table, int32_t r) -> bool {
@@ -518,8 +554,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
             rp[1] = ld_ahead_v4(rs + 8, r >= 0 && rope_d + 8 < p.d_rope);
           }
         };
-        load(checked(entry(0)));
-        int32_t v = entry(1);
+        load(checked(v0));
+        int32_t v = v1;
+        if (!bring_q()) break;
         for (int32_t b = 0; b < n_list; ++b) {
           // The next block's loads go out together after the announcement: a load among the uses of
           // this block's would share a scoreboard with loads still to be used, which then wait for
@@ -546,11 +583,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         }
       } else {
         const __nv_bfloat16* table = p.kv + seq * p.max_len * static_cast<int64_t>(d_qk);
-        int32_t v = entry(0);
+        int32_t v = v0, next = v1;
+        if (!bring_q()) break;
         for (int32_t b = 0; b < n_list && ok; ++b, ++nb) {
-          const int32_t next = entry(b + 1);
           ok = copy_block(table, checked(v));
           v = next;
+          next = entry(b + 2);
         }
       }
       if constexpr (kTree) {
@@ -576,7 +614,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     for (int32_t it = pair; it < p.n_items && ok; it += n_pairs, ++n_it) {
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
       if (!warp_wait(info_full(slot), sph, 10)) break;
-      const int32_t n_blocks = info_base[slot * C::INFO_WORDS] + info_base[slot * C::INFO_WORDS + 2];
+      const int32_t n_blocks = info_base[slot * C::INFO_WORDS] + info_base[slot * C::INFO_WORDS + 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(info_empty(slot));
       if (n_blocks == 0) continue;
@@ -680,7 +718,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
       if (!warp_wait(info_full(slot), sph, 20)) break;
       volatile int32_t* info = info_base + slot * C::INFO_WORDS;
-      const int32_t n_list = info[0], end = info[1], n_tail = info[2], k0 = info[3];
+      const int32_t n_list = info[0], n_tail = info[1], k0 = info[2];
       uint32_t path[kTree ? kMaxDraft / 64 : 1];         // this half's words of the drafted blocks
       if constexpr (kTree) {
 #pragma unroll
@@ -709,7 +747,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       const int32_t* idx_row = p.idx + static_cast<size_t>(m.qi) * p.topk;
       auto entry = [&](int32_t b) -> int32_t {
         const int32_t j = m.e0 + b * C::BLK + static_cast<int32_t>(32u * part + lane);
-        return b < n_list && j < end ? __ldg(idx_row + j) : -1;
+        return j < m.e1 ? __ldg(idx_row + j) : -1;
       };
       int32_t v = entry(0);
       float m2 = -INFINITY, l_r = 0.f, l_f = 0.f;        // running max; sums of rounded and unrounded weights
@@ -793,6 +831,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         } else if (nb >= 2) {
           if (!warp_wait(o_done(st), ((nb >> 1) & 1u) ^ 1u, 23)) { ok = false; break; }
         }
+        // the item before stored its outputs through the P buffers, each warp at its own pace
+        if (b == 0 && n_busy > 0 && !warp_wait(stored, (n_busy - 1) & 1u, 26)) { ok = false; break; }
         // ---- P row hl, columns 32 part .. +31: four chunks of the 128-byte swizzled row
         const uint32_t prow_at = sbase + C::OFF_P + st * C::P_BYTES;
 #pragma unroll
@@ -810,40 +850,69 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       ++n_busy;
       tc_fence_after();
       const float inv = l_r == 0.f ? 0.f : 1.0f / l_r;
+      // 32 dims of 32 heads at a time go through this warp's 4 KB of the P buffers (free now: the outputs
+      // that read them are done), so that a store instruction writes whole 128-byte (fp32) or 64-byte
+      // (bf16) pieces of rows; straight from the lanes, a row each, it took 10K clocks. The 16-byte chunks
+      // are swizzled so that eight lanes at a time, writing or reading, fall into distinct bank groups.
+      const uint32_t tile = sbase + C::OFF_P + warp * 4096u;
+      const int32_t head0 = static_cast<int32_t>(64u * rank + (warp & 1u) * 32u);       // of lane 0
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {                      // 2 instructions x 128 columns, 32 at a time
         const int32_t dim = 256 * (k >> 2) + 128 * static_cast<int32_t>(part) + 32 * (k & 3);
+        if (dim >= p.d_latent) break;                    // (rises with k)
         uint32_t o[32];
         tmem_ld32(tmem + lane_off + C::COL_O + 32 * k, o);
         tmem_wait_ld();
-        if (!writes) continue;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * inv);
+        __syncwarp();                                    // the previous pass has been read
         if (p.n_splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.d_latent + dim);
+          const uint32_t at = tile + (lane >> 1) * 128u;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            if (dim + 8 * u >= p.d_latent) break;
             uint32_t w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * x]) * inv,
-                                                              __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
+              const __nv_bfloat162 pr =
+                  __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * x]), __uint_as_float(o[8 * u + 2 * x + 1]));
               w[x] = *reinterpret_cast<const uint32_t*>(&pr);
             }
-            dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
+            st_shared_v4(at + ((((lane & 1u) * 4u + u) ^ ((lane >> 1) & 7u)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          __syncwarp();
+          const uint32_t ch = lane & 3u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t r = 8u * i + (lane >> 2);
+            const uint4 x = ld_shared_v4(tile + (r >> 1) * 128u + ((((r & 1u) * 4u + ch) ^ ((r >> 1) & 7u)) << 4));
+            const int32_t hd = head0 + static_cast<int32_t>(r), d = dim + 8 * static_cast<int32_t>(ch);
+            if (hd < p.n_heads && d < p.d_latent)
+              *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(m.qi) * p.n_heads + hd) * p.d_latent + d) = x;
           }
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_out + prow * p.d_latent + dim);
+          const uint32_t at = tile + lane * 128u;
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            if (dim + 4 * u >= p.d_latent) break;
-            dst[u] = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
-                                 __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+          for (int u = 0; u < 8; ++u)
+            st_shared_v4(at + ((u ^ (lane & 7u)) << 4), make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+          __syncwarp();
+          const uint32_t ch = lane & 7u;
+          float* base = p.part_out + (static_cast<size_t>(m.qi) * p.n_splits + m.split) * p.n_heads * p.d_latent;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t r = 4u * i + (lane >> 3);
+            const uint4 x = ld_shared_v4(tile + r * 128u + ((ch ^ (r & 7u)) << 4));
+            const int32_t hd = head0 + static_cast<int32_t>(r), d = dim + 4 * static_cast<int32_t>(ch);
+            if (hd < p.n_heads && d < p.d_latent)
+              *reinterpret_cast<uint4*>(base + static_cast<size_t>(hd) * p.d_latent + d) = x;
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_leader(o_empty);
+      if (lane == 0) {
+        mbar_arrive(stored);
+        arrive_leader(o_empty);
+      }
       if (writes && part == 0) {
         const float l2 = l_f == 0.f ? -INFINITY : m2 + log2f(l_f);
         if (p.n_splits == 1) p.lse[row] = l2 * 0.69314718055994531f;
