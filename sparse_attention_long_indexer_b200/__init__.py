@@ -118,13 +118,20 @@ def _ptr(t: Optional[torch.Tensor]):
         return None
     if not t.is_contiguous():
         raise ValueError("DSA tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# The current stream's handle without a torch.cuda.Stream object around it (3 us of every call), where
+# this torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(status: int, where: str):
@@ -330,21 +337,22 @@ def forward(dims, q_idx, w, k_idx, q_scale, k_scale, lengths, topk, q, latent_kv
 _SCALE_GROUP = 128      # latent dims per scale
 
 
-def _same(name: str, t: torch.Tensor, dtype, numel: int, device):
-    """Checks one tensor of a call: dtype, size, device and layout, so that no kernel reads past its end."""
-    if t.dtype != dtype:
+def _same(name: str, t: torch.Tensor, dtype, numel: int, device: int):
+    """Checks one tensor of a call: dtype, size and device, so that no kernel reads past its end."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{name}: expected {numel} elements, got {t.numel()} in {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{device}")
 
 
-def _call_device(t: torch.Tensor) -> torch.device:
+def _call_device(t: torch.Tensor) -> int:
     """The device of a call's tensors, which must be the current one (its stream takes the launch)."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    device = t.get_device()                       # -1 on the CPU
+    if device < 0 or device != torch.cuda.current_device():
         raise ValueError(f"tensors on {t.device}: make it the current device first (torch.cuda.device)")
-    return t.device
+    return device
 
 
 @dataclass
@@ -423,7 +431,7 @@ def qcache_read(dims, cache: QCache, ws: Workspace, rows=None, start=None, lengt
     if rows is not None:
         _same("rows", rows, torch.int32, dims.batch * dims.n_q, device)
     _per_sequence(dims, device, start=start, lengths=lengths)
-    out = torch.empty((dims.batch, dims.n_q, dims.d_latent + dims.d_rope), dtype=torch.bfloat16, device=device)
+    out = cache.rope.new_empty((dims.batch, dims.n_q, dims.d_latent + dims.d_rope))
     dsa_qcache_read(dims, cache._struct(dims, device), rows, start, lengths, out, ws.buf, stream)
     return out
 
@@ -433,8 +441,8 @@ def _attention_inputs(dims, q, idx, topk, ws):
     queries = dims.batch * dims.n_q
     _same("q", q, torch.bfloat16, queries * dims.n_heads * (dims.d_latent + dims.d_rope), device)
     _same("idx", idx, torch.int32, queries * topk, device)
-    out = torch.empty((dims.batch, dims.n_q, dims.n_heads, dims.d_latent), dtype=torch.bfloat16, device=device)
-    lse = torch.empty((dims.batch, dims.n_q, dims.n_heads), dtype=torch.float32, device=device)
+    out = q.new_empty((dims.batch, dims.n_q, dims.n_heads, dims.d_latent))
+    lse = q.new_empty((dims.batch, dims.n_q, dims.n_heads), dtype=torch.float32)
     return device, out, lse
 
 
