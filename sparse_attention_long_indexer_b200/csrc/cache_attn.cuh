@@ -18,7 +18,8 @@
 // which needs no cluster but computes and expands everything for the logits twice, took 1.67 ms for
 // 1024 queries of 2048 rows.)
 //
-// One CTA, 22 warps:
+// One CTA, 23 warps:
+//  * control (1 warp): how far the range's list reaches, a node's path, and the item's q, ahead of the item.
 //  * producers: 8 warps bring this CTA's 32 rows of each block, all dims (the logits' operand), 8 warps
 //    all 64 rows' dims that it supplies to the output; each part has a 2-stage ring of
 //    128-byte-swizzled bf16 tiles. 8-bit rows are loaded into registers one block ahead and expanded
@@ -60,7 +61,8 @@ struct CacheAttnCfg {
   static constexpr int PRODUCER_WARPS = 2 * PART_WARPS;
   static constexpr int S_WARP = SOFTMAX_WARPS + PRODUCER_WARPS;   // logits MMAs (and TMEM owner)
   static constexpr int O_WARP = S_WARP + 1;                       // output MMAs
-  static constexpr int THREADS = (O_WARP + 1) * 32;
+  static constexpr int CTRL_WARP = S_WARP + 2;
+  static constexpr int THREADS = (CTRL_WARP + 1) * 32;
   // TMEM columns
   static constexpr uint32_t COL_O = 0, COL_S = 256, COL_Q = COL_S + 32 * S_BUFS, TMEM_COLS = 512;
   // shared memory
@@ -208,8 +210,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto B = [&](uint32_t i) { return bar0 + 8u * i; };
   // in both CTAs
-  auto info_full = [&](uint32_t i) { return B(0 + i); };     // first producer warp
-  auto info_empty = [&](uint32_t i) { return B(2 + i); };    // everyone else who reads info
+  auto info_full = [&](uint32_t i) { return B(0 + i); };     // control warp
+  auto info_empty = [&](uint32_t i) { return B(2 + i); };    // everyone who reads info
   auto s_full = [&](uint32_t i) { return B(4 + i); };        // commit (3): logits of a block done, its part read
   auto o_done = [&](uint32_t j) { return B(7 + j); };        // commit (2): outputs of a block done, its part and P read
   const uint32_t o_full = B(9);                              // commit: the item's outputs are done
@@ -237,8 +239,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(info_full(i), 1);
-      // softmax and producer warps (without the first), and the MMA warps (odd CTA: the relay)
-      mbar_init(info_empty(i), C::SOFTMAX_WARPS + C::PRODUCER_WARPS - 1 + (leader ? 2 : 1));
+      // softmax and producer warps, and the MMA warps (odd CTA: the relay)
+      mbar_init(info_empty(i), C::SOFTMAX_WARPS + C::PRODUCER_WARPS + (leader ? 2 : 1));
       mbar_init(o_done(i), 1);
       mbar_init(p_local(i), C::SOFTMAX_WARPS);
       mbar_init(l_full(i), 2 * C::PART_WARPS);
@@ -283,21 +285,12 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     if (leader) mbar_arrive(bar);
     else mbar_arrive_cluster(bar + lead_off);
   };
-  // Lane 0 waits for the warp. The warp barrier orders the other lanes' accesses behind its acquire (the
-  // shuffle alone does not: their loads may be moved above it).
+  // Every lane waits (each one's own acquire orders its accesses) and the warp goes on, or gives up, as one.
   auto warp_wait = [&](uint32_t bar, uint32_t parity, uint32_t tag) -> bool {
-    uint32_t got = 1;
-    if (lane == 0) got = wt.wait(bar, parity, tag) ? 1u : 0u;
-    got = __shfl_sync(0xffffffffu, got, 0);
-    __syncwarp();
-    return got != 0;
+    return __all_sync(0xffffffffu, wt.wait(bar, parity, tag));
   };
   auto warp_wait_pair = [&](uint32_t bar, uint32_t parity, uint32_t tag) -> bool {
-    uint32_t got = 1;
-    if (lane == 0) got = wt.template wait<true>(bar, parity, tag) ? 1u : 0u;
-    got = __shfl_sync(0xffffffffu, got, 0);
-    __syncwarp();
-    return got != 0;
+    return __all_sync(0xffffffffu, wt.template wait<true>(bar, parity, tag));
   };
 
   // item -> (query, range of its rows)
@@ -346,12 +339,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       return logits_part ? (2u * k + (c >> 2)) * C::L_ATOM : static_cast<uint32_t>(k) * C::O_ATOM;
     };
     uint32_t n_it = 0, n_busy = 0, nb = 0;                   // items, items with blocks, blocks so far
-    bool tma_pending = false;
     for (int32_t it = pair; it < p.n_items; it += n_pairs, ++n_it) {
       const Item m = item_of(it);
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
       volatile int32_t* info = info_base + slot * C::INFO_WORDS;
-      const int32_t node = m.qi % p.n_q;
       const int64_t seq = m.qi / p.n_q;
       const int32_t* idx_row = p.idx + static_cast<size_t>(m.qi) * p.topk;
       // this thread's entry of list block b (read ahead of its use), and the row it stands for, or -1.
@@ -366,64 +357,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         return -1;
       };
       const int32_t v0 = entry(0), v1 = entry(1);
-      if (pw == 0) {
-        // ---- the extent of the list in this range (one past its last entry >= 0, found from the
-        // end), and the node's path through the tree
-        if (!warp_wait(info_empty(slot), sph ^ 1u, 1)) break;
-        int32_t end = m.e0;
-        for (int32_t hi = m.e1; hi > m.e0 && end == m.e0;) {
-          const int32_t lo = max(m.e0, hi - 256);
-          int32_t last = m.e0 - 1;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int32_t j = lo + static_cast<int32_t>(lane) + 32 * i;
-            if (j < hi && __ldg(idx_row + j) >= 0) last = j;
-          }
-          end = __reduce_max_sync(0xffffffffu, last) + 1;
-          hi = lo;
-        }
-        int32_t n_list = (end - m.e0 + C::BLK - 1) / C::BLK, n_tail = 0;
-        if constexpr (kTree) {
-          const int32_t* par_row = p.parents + seq * p.n_q;
-          int32_t par[kMaxDraft / 32];
-#pragma unroll
-          for (int w = 0; w < kMaxDraft / 32; ++w) {
-            const int32_t j = 32 * w + static_cast<int32_t>(lane);
-            par[w] = j < p.n_q ? __ldg(par_row + j) : -2;
-          }
-          uint32_t path = 0;                             // lane w: bits of nodes 32w .. 32w+31
-          int32_t cur = node;
-          bool present = true;
-          while (true) {                                 // cur falls strictly: at most n_q steps
-            int32_t v = par[0];
-#pragma unroll
-            for (int w = 1; w < kMaxDraft / 32; ++w)
-              if ((cur >> 5) == w) v = par[w];
-            v = __shfl_sync(0xffffffffu, v, cur & 31);
-            if (static_cast<int32_t>(lane) == (cur >> 5)) path |= 1u << (cur & 31);
-            if (v >= cur) {                              // not an earlier node
-              if (lane == 0) record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(m.qi));
-              present = false;
-            } else if (v < -1) {
-              present = false;
-            }
-            if (!present || v < 0) break;
-            cur = v;
-          }
-          n_tail = max(0, min(m.k1, node / C::BLK + 1) - m.k0);
-          if (!present) n_list = n_tail = 0;             // an absent node, or one below an absent node
-          if (lane < kMaxDraft / 32) info[4 + lane] = static_cast<int32_t>(path);
-        }
-        if (lane == 0) {
-          info[0] = n_list;
-          info[1] = n_tail;
-          info[2] = m.k0;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(info_full(slot));
-      } else {
-        if (!warp_wait(info_full(slot), sph, 2)) break;
-      }
+      if (!warp_wait(info_full(slot), sph, 2)) break;
       const int32_t n_list = info[0], n_tail = info[1], k0 = info[2];
       uint32_t path = 0;                                 // bit k: this thread's row of drafted block k0 + k is attended
       if constexpr (kTree) {
@@ -431,30 +365,15 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
           path |= ((static_cast<uint32_t>(info[4 + 2 * (k0 + k) + (block_row >> 5)]) >> (block_row & 31)) & 1u) << k;
       }
       __syncwarp();
-      if (pw != 0 && lane == 0) mbar_arrive(info_empty(slot));
+      if (lane == 0) mbar_arrive(info_empty(slot));
       if (n_list + n_tail == 0) continue;
 
-      // ---- q, once the previous item's logits MMAs have read theirs: all dims by TMA, dims 320.. where
-      // they stay, dims 0..319 into the logits ring, which is free then, and from there into the
-      // TMEM lanes (both lane halves hold this CTA's 64 heads; every producer warp a lane quarter and
-      // 80 dims). A load per lane straight from global memory touches a line each and took 5K clocks.
-      // Past the query's last dim TMA fills zeros; rows past its last head only reach unused lanes.
+      // ---- q: it lands in shared memory (see the control warp); its dims 0..319 go from the logits ring,
+      // which is free then, into the TMEM lanes (both lane halves hold this CTA's 64 heads; every producer
+      // warp a lane quarter and 80 dims). A load per lane straight from global memory touches a line each
+      // and took 5K clocks.
       const uint32_t q_par = n_busy & 1u;
       ++n_busy;
-      if (pw == 0) {
-        if (!warp_wait(q_empty, q_par ^ 1u, 3)) break;
-        if (lane == 0) {
-          const int32_t atoms = (d_qk + 63) / 64;
-          fence_proxy_async_smem();                        // the ring's earlier stores before TMA's
-          mbar_expect_tx(q_tma, static_cast<uint32_t>(atoms) * C::Q_ATOM);
-          tma_pending = true;
-          for (int32_t t = 0; t < atoms; ++t)
-            tma_load_3d(sbase + (t < C::Q_TMEM_DIMS / 64 ? C::OFF_L + t * C::Q_ATOM
-                                                         : C::OFF_QS + (t - C::Q_TMEM_DIMS / 64) * C::Q_ATOM),
-                        &map_q, q_tma, 64 * t, m.qi * p.n_heads + 64 * static_cast<int32_t>(rank), 0);
-        }
-        __syncwarp();
-      }
       auto bring_q = [&]() -> bool {
         if (!warp_wait(q_tma, q_par, 4)) return false;
         tc_fence_after();
@@ -599,8 +518,89 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       if (!ok) break;
     }
     cp_async_wait<0>();
+  } else if (warp == static_cast<uint32_t>(C::CTRL_WARP)) {
+    // ================================================================ control: an item's extent, path and q, ahead of it
+    uint32_t n_it = 0, n_busy = 0;
+    for (int32_t it = pair; it < p.n_items; it += n_pairs, ++n_it) {
+      const Item m = item_of(it);
+      const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
+      volatile int32_t* info = info_base + slot * C::INFO_WORDS;
+      const int32_t node = m.qi % p.n_q;
+      const int64_t seq = m.qi / p.n_q;
+      const int32_t* idx_row = p.idx + static_cast<size_t>(m.qi) * p.topk;
+      // ---- the extent of the list in this range (one past its last entry >= 0, found from the
+      // end), and the node's path through the tree
+      if (!warp_wait(info_empty(slot), sph ^ 1u, 1)) break;
+      int32_t end = m.e0;
+      for (int32_t hi = m.e1; hi > m.e0 && end == m.e0;) {
+        const int32_t lo = max(m.e0, hi - 256);
+        int32_t last = m.e0 - 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t j = lo + static_cast<int32_t>(lane) + 32 * i;
+          if (j < hi && __ldg(idx_row + j) >= 0) last = j;
+        }
+        end = __reduce_max_sync(0xffffffffu, last) + 1;
+        hi = lo;
+      }
+      int32_t n_list = (end - m.e0 + C::BLK - 1) / C::BLK, n_tail = 0;
+      if constexpr (kTree) {
+        const int32_t* par_row = p.parents + seq * p.n_q;
+        int32_t par[kMaxDraft / 32];
+#pragma unroll
+        for (int w = 0; w < kMaxDraft / 32; ++w) {
+          const int32_t j = 32 * w + static_cast<int32_t>(lane);
+          par[w] = j < p.n_q ? __ldg(par_row + j) : -2;
+        }
+        uint32_t path = 0;                             // lane w: bits of nodes 32w .. 32w+31
+        int32_t cur = node;
+        bool present = true;
+        while (true) {                                 // cur falls strictly: at most n_q steps
+          int32_t v = par[0];
+#pragma unroll
+          for (int w = 1; w < kMaxDraft / 32; ++w)
+            if ((cur >> 5) == w) v = par[w];
+          v = __shfl_sync(0xffffffffu, v, cur & 31);
+          if (static_cast<int32_t>(lane) == (cur >> 5)) path |= 1u << (cur & 31);
+          if (v >= cur) {                              // not an earlier node
+            if (lane == 0) record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(m.qi));
+            present = false;
+          } else if (v < -1) {
+            present = false;
+          }
+          if (!present || v < 0) break;
+          cur = v;
+        }
+        n_tail = max(0, min(m.k1, node / C::BLK + 1) - m.k0);
+        if (!present) n_list = n_tail = 0;             // an absent node, or one below an absent node
+        if (lane < kMaxDraft / 32) info[4 + lane] = static_cast<int32_t>(path);
+      }
+      if (lane == 0) {
+        info[0] = n_list;
+        info[1] = n_tail;
+        info[2] = m.k0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(info_full(slot));
+      // ---- q, once the previous item's logits MMAs have read theirs: all dims by TMA, dims 320.. where they
+      // stay, dims 0..319 into the logits ring. Past the query's last dim TMA fills zeros; rows past its
+      // last head only reach unused lanes.
+      if (n_list + n_tail == 0) continue;
+      if (!warp_wait(q_empty, (n_busy & 1u) ^ 1u, 3)) break;
+      ++n_busy;
+      if (lane == 0) {
+        const int32_t atoms = (d_qk + 63) / 64;
+        fence_proxy_async_smem();                          // the ring's earlier stores before TMA's
+        mbar_expect_tx(q_tma, static_cast<uint32_t>(atoms) * C::Q_ATOM);
+        for (int32_t t = 0; t < atoms; ++t)
+          tma_load_3d(sbase + (t < C::Q_TMEM_DIMS / 64 ? C::OFF_L + t * C::Q_ATOM
+                                                       : C::OFF_QS + (t - C::Q_TMEM_DIMS / 64) * C::Q_ATOM),
+                      &map_q, q_tma, 64 * t, m.qi * p.n_heads + 64 * static_cast<int32_t>(rank), 0);
+      }
+      __syncwarp();
+    }
     // after an abort the q copy in flight lands before the CTA may leave (else it has landed)
-    if (tma_pending && wt.aborted()) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
+    if (lane == 0 && n_busy > 0 && wt.aborted()) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
   } else if (warp >= static_cast<uint32_t>(C::S_WARP)) {
     // ================================================================ MMA issuers (even CTA), relay (odd CTA)
     // One warp issues the logits MMAs, one the output MMAs, so that each one's waits (issue blocks
