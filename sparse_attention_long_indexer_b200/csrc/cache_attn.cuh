@@ -293,6 +293,14 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     return __all_sync(0xffffffffu, wt.template wait<true>(bar, parity, tag));
   };
 
+  // the logits buffer of the next block, and the parity of that use
+  auto advance = [](uint32_t& buf, uint32_t& par) {
+    if (++buf == static_cast<uint32_t>(C::S_BUFS)) {
+      buf = 0;
+      par ^= 1u;
+    }
+  };
+
   // item -> (query, range of its rows)
   struct Item {
     int32_t qi, split;
@@ -339,6 +347,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       return logits_part ? (2u * k + (c >> 2)) * C::L_ATOM : static_cast<uint32_t>(k) * C::O_ATOM;
     };
     uint32_t n_it = 0, n_busy = 0, nb = 0;                   // items, items with blocks, blocks so far
+    uint32_t s_buf = 0, s_par = 0;                           // logits buffer of block nb - 2, and its use's parity
     for (int32_t it = pair; it < p.n_items; it += n_pairs, ++n_it) {
       const Item m = item_of(it);
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
@@ -415,7 +424,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         const uint32_t st = nb & 1u;
         if (logits_part) {                                 // last read by the logits of block nb - 2
           tile = sbase + C::OFF_L + st * C::L_BYTES;
-          return nb < 2 || warp_wait(s_full((nb - 2) % C::S_BUFS), ((nb - 2) / C::S_BUFS) & 1u, 5);
+          if (nb < 2) return true;
+          const uint32_t bar = s_full(s_buf), par = s_par;
+          advance(s_buf, s_par);
+          return warp_wait(bar, par, 5);
         }
         tile = sbase + C::OFF_O + st * C::O_BYTES;
         return warp_wait(o_done(st), ((nb >> 1) & 1u) ^ 1u, 6);
@@ -610,6 +622,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     const bool logits = warp == static_cast<uint32_t>(C::S_WARP);
     const int32_t out_instr = p.d_latent > 256 ? 2 : 1;
     uint32_t n_it = 0, n_busy = 0, nb = 0;
+    uint32_t buf = 0, buf_par = 0;                       // logits buffer, and the parity of its use
     bool ok = leader || logits;                          // the odd CTA's second warp has nothing to do
     for (int32_t it = pair; it < p.n_items && ok; it += n_pairs, ++n_it) {
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
@@ -629,9 +642,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       } else if (logits) {
         if (!warp_wait_pair(q_full, n_busy & 1u, 12)) break;
         for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
-          const uint32_t st = nb & 1u, buf = nb % C::S_BUFS;
+          const uint32_t st = nb & 1u;
           if (!warp_wait_pair(l_full(st), (nb >> 1) & 1u, 13)) { ok = false; break; }
-          if (!warp_wait(s_free(buf), ((nb / C::S_BUFS) & 1u) ^ 1u, 14)) { ok = false; break; }
+          if (!warp_wait(s_free(buf), buf_par ^ 1u, 14)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tmem + C::COL_S + 32u * buf;
           const uint64_t tile = sw128_desc(sbase + C::OFF_L + st * C::L_BYTES, 1, 1024);
@@ -652,6 +665,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
             commit_pair(s_full(buf));
           }
           __syncwarp();
+          advance(buf, buf_par);
         }
         if (!ok) break;
         if (elect_one()) commit_pair(q_empty);
@@ -661,8 +675,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
           const uint32_t st = nb & 1u;
           if (!warp_wait_pair(v_full(st), (nb >> 1) & 1u, 16)) { ok = false; break; }
           if (!warp_wait_pair(p_full(st), (nb >> 1) & 1u, 17)) { ok = false; break; }
-          if (lane == 0) mbar_arrive(s_free(nb % C::S_BUFS));    // the softmax is done with that logits buffer
+          if (lane == 0) mbar_arrive(s_free(buf));       // the softmax is done with that logits buffer
           __syncwarp();
+          advance(buf, buf_par);
           tc_fence_after();
           const uint64_t pd = sw128_desc(sbase + C::OFF_P + st * C::P_BYTES, 1, 1024);
           const uint64_t tile = sw128_desc(sbase + C::OFF_O + st * C::O_BYTES, C::O_ATOM, 1024);
@@ -698,6 +713,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     const uint32_t lane_off = (warp * 32u) << 16;
     const float sc = p.scale_log2;
     uint32_t n_it = 0, n_busy = 0, nb = 0, nx = 0;
+    uint32_t buf = 0, buf_par = 0;                       // logits buffer, and the parity of its use
     bool ok = true;
     // One float from the thread with the other half of the row. Each thread has two words and stores
     // (number, value) in one; a word is used again only after the partner has answered the next
@@ -752,7 +768,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       int32_t v = entry(0);
       float m2 = -INFINITY, l_r = 0.f, l_f = 0.f;        // running max; sums of rounded and unrounded weights
       for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
-        const uint32_t buf = nb % C::S_BUFS, st = nb & 1u;
+        const uint32_t st = nb & 1u;
         uint32_t vm = __ballot_sync(0xffffffffu, v >= 0 && v < p.max_len);
         if constexpr (kTree) {
           if (b >= n_list) {
@@ -763,12 +779,13 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
           }
         }
         v = entry(b + 1);
-        if (!warp_wait(s_full(buf), (nb / C::S_BUFS) & 1u, 21)) { ok = false; break; }
+        if (!warp_wait(s_full(buf), buf_par, 21)) { ok = false; break; }
         tc_fence_after();
         uint32_t z[32];
         tmem_ld32(tmem + lane_off + C::COL_S + 32u * buf, z);
         tmem_wait_ld();
         tc_fence_before();
+        advance(buf, buf_par);
         if (vm != 0xffffffffu) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
