@@ -153,6 +153,10 @@ __device__ __forceinline__ float ld_ahead_f32(const float* src, bool in) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // Bounded waits on the SM's own clock. (The wait of ptx.cuh takes its time from %globaltimer, whose
 // first read, about a thousand clocks, every wait that is not over at once would pay.) Same contract:
 // past the budget the error is recorded and the CTA's abort flag raised, and every later wait fails.
@@ -232,6 +236,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   const uint32_t stored = B(27);                             // softmax warps: an item's outputs are out of the P buffers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);   // blocks read by the softmax
 
   const uint32_t warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_ctarank();
@@ -260,6 +265,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     mbar_init(o_empty, 2 * C::SOFTMAX_WARPS);
     mbar_init(mma_done, 2);
     *abort_flag = 0;
+    *progress = 0;
     fence_mbar_init();
     prefetch_tensormap(&map_q);
   }
@@ -532,7 +538,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     cp_async_wait<0>();
   } else if (warp == static_cast<uint32_t>(C::CTRL_WARP)) {
     // ================================================================ control: an item's extent, path and q, ahead of it
-    uint32_t n_it = 0, n_busy = 0;
+    uint32_t n_it = 0, n_busy = 0, nb = 0;
     for (int32_t it = pair; it < p.n_items; it += n_pairs, ++n_it) {
       const Item m = item_of(it);
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
@@ -610,6 +616,34 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
                       &map_q, q_tma, 64 * t, m.qi * p.n_heads + 64 * static_cast<int32_t>(rank), 0);
       }
       __syncwarp();
+      if constexpr (kQuant) {
+        // ---- this CTA's rows into L2, kAhead blocks before the logits come to them (lane = row). Paced by the
+        // softmax's count of blocks, which only grows: a barrier's parity would not do for a warp that
+        // nothing keeps from falling behind.
+        constexpr int32_t kAhead = 4;
+        const int32_t groups = (p.d_latent + kScaleGroup - 1) / kScaleGroup;
+        const uint32_t row0 = static_cast<uint32_t>(seq) * static_cast<uint32_t>(p.max_len);
+        for (int32_t b = 2; b < n_list; ++b) {
+          const int32_t j = m.e0 + b * C::BLK + static_cast<int32_t>(32u * rank + lane);
+          const int32_t v = j < m.e1 ? __ldg(idx_row + j) : -1;
+          uint32_t spins = 0;
+          int64_t t0 = 0;
+          bool ok = true;
+          while (ok && static_cast<int32_t>(nb + b - kAhead - *progress) > 0) {
+            __nanosleep(200);
+            ok = wt.again(spins, t0, 8);
+          }
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (v >= 0 && v < p.max_len) {
+            const uint64_t r = row0 + static_cast<uint32_t>(v);
+            const uint8_t* codes = p.cache.codes + r * static_cast<uint32_t>(p.d_latent);
+            for (int32_t d = 0; d < p.d_latent; d += 128) prefetch_l2(codes + d);
+            prefetch_l2(p.cache.scales + r * static_cast<uint32_t>(groups));
+            if (p.d_rope > 0) prefetch_l2(p.cache.rope + r * static_cast<uint32_t>(p.d_rope));
+          }
+        }
+        nb += static_cast<uint32_t>(n_list + n_tail);
+      }
     }
     // after an abort the q copy in flight lands before the CTA may leave (else it has landed)
     if (lane == 0 && n_busy > 0 && wt.aborted()) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
@@ -786,6 +820,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         tmem_wait_ld();
         tc_fence_before();
         advance(buf, buf_par);
+        if (kQuant && threadIdx.x == 0) *progress = nb + 1;
         if (vm != 0xffffffffu) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
