@@ -238,6 +238,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 8);   // blocks read by the softmax
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // a join behind this kernel waits for its end itself
   const uint32_t warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -991,6 +992,7 @@ constexpr int kJoinThreads = 128;
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(
     const float* __restrict__ part_out, const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ out,
     float* __restrict__ lse, int32_t n_splits, int32_t n_heads, int32_t d_latent) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");    // the ranges' kernel is done and its stores are visible
   const int64_t row = blockIdx.x;                        // (query, head)
   const int64_t qi = row / n_heads, head = row - qi * n_heads;
   const float* lrow = part_lse + qi * n_splits * n_heads + head;
@@ -1000,7 +1002,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(
   const float msub = mx == -INFINITY ? 0.f : mx;
   const int32_t dim = 4 * static_cast<int32_t>(threadIdx.x);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int32_t s = 0; s < n_splits; ++s) {
     const float l = __ldg(lrow + static_cast<int64_t>(s) * n_heads);
     const float w = exp2f(l - msub);

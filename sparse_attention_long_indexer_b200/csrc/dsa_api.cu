@@ -830,14 +830,17 @@ int row_grid(int64_t rows, int sms) {
   return static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, static_cast<int64_t>(8) * sms));
 }
 
-// How the rows of a query are split (see cache_attn.cuh). The cost of a split is what the slowest
-// pair of SMs does: its items one after another, each a fixed part (q, statistics, output) and its blocks,
-// and, with more than one range, the join: a launch, and the ranges' outputs written and read.
+// How the rows of a query are split (see cache_attn.cuh): by the least cost of the slowest pair of SMs,
+// whose items follow one another, and of the join. Measured at the production dims: an item takes 9 us
+// beside its blocks (list, q, first loads, output) and 1.87 us per block; a join 2 us, 0.1 us per range
+// of a query and 0.05 us per range of all queries (256 KB written and read). One query of 2048 rows in
+// 1 / 8 / 16 / 32 ranges: 72.8 / 22.6 / 19.9 / 21.7 us; 16 queries in 1 / 4 / 8: 73.9 / 34.6 / 40.5 us;
+// 64 queries in 1 / 2: 78 / 94 us. The pairs are this rule's, not the device's: it also sizes workspaces.
 struct CachePlan {
   int32_t n_splits, split_blocks;
 };
 constexpr int64_t kPlanPairs = 74;
-constexpr int64_t kPlanItemNs = 2500, kPlanBlockNs = 1200, kPlanJoinNs = 3000, kPlanPartNs = 130;
+constexpr int64_t kPlanItemNs = 9000, kPlanBlockNs = 1870, kPlanJoinNs = 2000, kPlanRangeNs = 100, kPlanPartNs = 50;
 CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
   CachePlan best{1, 1};
   const int64_t queries = static_cast<int64_t>(d.batch) * d.n_q;
@@ -850,7 +853,7 @@ CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
     if (least >= 0 && splits == best.n_splits) continue;
     const int64_t waves = (queries * splits + kPlanPairs - 1) / kPlanPairs;
     int64_t cost = waves * (kPlanItemNs + per * kPlanBlockNs);
-    if (splits > 1) cost += kPlanJoinNs + kPlanPartNs * queries * splits;
+    if (splits > 1) cost += kPlanJoinNs + kPlanRangeNs * splits + kPlanPartNs * queries * splits;
     if (least < 0 || cost < least) {
       least = cost;
       best.n_splits = splits;
@@ -940,9 +943,19 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   else if (tree) s = launch_cache_attn<true, true>(map_q, p, dev.sms, st);
   else s = launch_cache_attn<true, false>(map_q, p, dev.sms, st);
   if (s != DSA_OK || plan.n_splits == 1) return s;
-  cache_attn_join_kernel<<<static_cast<unsigned>(queries * d.n_heads), kJoinThreads, 0, st>>>(
-      p.part_out, p.part_lse, p.out, p.lse, plan.n_splits, d.n_heads, d.d_latent);
-  return from_cuda(cudaGetLastError());
+  // the join may be set up while the ranges still run: it waits for them (griddepcontrol) before it reads
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(queries * d.n_heads));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return from_cuda(cudaLaunchKernelEx(&cfg, cache_attn_join_kernel, static_cast<const float*>(p.part_out),
+                                      static_cast<const float*>(p.part_lse), p.out, p.lse, plan.n_splits, d.n_heads,
+                                      d.d_latent));
 }
 
 }  // namespace
