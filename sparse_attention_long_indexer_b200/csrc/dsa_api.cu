@@ -825,9 +825,9 @@ dsa_status check_status_ws(void* ws, size_t ws_bytes) {
   return ws == nullptr || !aligned(ws, kAlign) || ws_bytes < kAlign ? DSA_ERR_WORKSPACE : DSA_OK;
 }
 
-// One warp per row, as many CTAs as there are rows for up to 8 resident ones per SM.
+// One warp per row, as many CTAs as there are rows for, up to those that fit at once.
 int row_grid(int64_t rows, int sms) {
-  return static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, static_cast<int64_t>(8) * sms));
+  return static_cast<int>(std::min<int64_t>((rows + kRowWarps - 1) / kRowWarps, static_cast<int64_t>(kRowCtas) * sms));
 }
 
 // How the rows of a query are split (see cache_attn.cuh): by the least cost of the slowest pair of SMs,

@@ -25,6 +25,10 @@ constexpr int kScaleGroup = 128;         // latent dims per scale
 constexpr int kScaleExpMax = 100;        // |exponent| of a scale
 constexpr int kRowThreads = 256;         // 8 warps = 8 rows per CTA and pass
 constexpr int kRowWarps = kRowThreads / 32;
+// Resident CTAs per SM, and the most that are launched. 32768 rows written take 16.3 us (4.4 TB/s of the
+// 6.5 a copy reaches); with 8 launched per SM, of which 6 fit, 18.3, and with the next row's loads ahead of
+// the current row's stores, at 4 per SM, 18.2.
+constexpr int kRowCtas = 6;
 
 struct QCacheView {
   uint8_t* codes;        // E4M3 [B, max_len, d_latent]
@@ -33,15 +37,22 @@ struct QCacheView {
 };
 
 // ------------------------------------------------------------------------- conversions
-// Largest finite magnitude of two packed bf16, as bit patterns (they order like the magnitudes).
+// Bit patterns of bf16 magnitudes order like the magnitudes; from kNonFinite on they are no numbers.
+constexpr uint32_t kNonFinite = 0x7F80u;
+// Two packed magnitudes, those of infinities and NaN replaced by zero.
 __device__ __forceinline__ uint32_t finite_mag2(uint32_t v) {
   uint32_t m = v & 0x7FFF7FFFu;
-  if ((m & 0xFFFFu) >= 0x7F80u) m &= 0xFFFF0000u;
-  if ((m >> 16) >= 0x7F80u) m &= 0x0000FFFFu;
+  if ((m & 0xFFFFu) >= kNonFinite) m &= 0xFFFF0000u;
+  if ((m >> 16) >= kNonFinite) m &= 0x0000FFFFu;
   return m;
 }
-__device__ __forceinline__ bool has_nan2(uint32_t v) {
-  return (v & 0x7FFFu) > 0x7F80u || ((v >> 16) & 0x7FFFu) > 0x7F80u;
+__device__ __forceinline__ uint32_t max4(const uint4& v, uint32_t mask) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & mask, v.y & mask), __vmaxu2(v.z & mask, v.w & mask));
+  return max(m & 0xFFFFu, m >> 16);
+}
+__device__ __forceinline__ uint32_t max4_finite(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(finite_mag2(v.x), finite_mag2(v.y)), __vmaxu2(finite_mag2(v.z), finite_mag2(v.w)));
+  return max(m & 0xFFFFu, m >> 16);
 }
 // Exponent of the scale from the bf16 bit pattern of amax: 448 = 1.75 * 2^8, so the smallest e
 // is (exponent of amax) - 8, one more where amax's significand is above 1.75 (mantissa 0x60).
@@ -53,17 +64,6 @@ __device__ __forceinline__ int scale_exp(uint32_t amax_bits) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-// Two packed bf16 times `inv`, rounded to E4M3 (to nearest even, magnitudes held to 448).
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t v, float inv) {
-  const float lo = __uint_as_float(v << 16) * inv, hi = __uint_as_float(v & 0xFFFF0000u) * inv;
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, float inv) {
-  return e4m3x2(a, inv) | (e4m3x2(b, inv) << 16);
-}
-
 // Two fp32 in one 64-bit register, for the packed fp32 instructions.
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
   uint64_t v;
@@ -72,6 +72,21 @@ __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
 }
 __device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// Four bf16 (two words) times `inv` (packed twice), rounded to E4M3 (to nearest even, magnitudes held to 448).
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, uint64_t inv2) {
+  uint64_t x = pack_f32x2(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+  uint64_t y = pack_f32x2(__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(inv2));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(inv2));
+  float x0, x1, y0, y1;
+  unpack_f32x2(x, x0, x1);
+  unpack_f32x2(y, y0, y1);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r) : "f"(x0), "f"(x1), "f"(y0), "f"(y1));
+  return r;
 }
 // Two E4M3 codes times a scale (packed twice), as two bf16. Codes convert to fp16 and fp16 to fp32
 // exactly; the product with a power of two, and its bf16 form, are exact too. 16 codes a word of four
@@ -118,71 +133,80 @@ struct QCacheWriteParams {
   int64_t rows;                  // B * n
 };
 
-__device__ __forceinline__ uint32_t group_max(uint32_t m, int width) {
-  for (int o = width >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+template <int kWidth>
+__device__ __forceinline__ uint32_t group_max(uint32_t m) {
+#pragma unroll
+  for (int o = kWidth / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
-__global__ void __launch_bounds__(kRowThreads) qcache_write_kernel(const QCacheWriteParams p) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) qcache_write_kernel(const QCacheWriteParams p) {
   const uint32_t lane = lane_id();
   const int groups = (p.d_latent + kScaleGroup - 1) / kScaleGroup;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp_id(); row < p.rows;
-       row += static_cast<int64_t>(gridDim.x) * kRowWarps) {
-    const int64_t b = row / p.n;
-    const int32_t j = static_cast<int32_t>(row - b * p.n);
+  const bool has_lat = p.latent != nullptr && static_cast<int32_t>(16 * lane) < p.d_latent;
+  const bool has_rope = p.latent != nullptr && static_cast<int32_t>(8 * lane) < p.d_rope;
+  const bool has_key = p.keys != nullptr && static_cast<int32_t>(8 * lane) < p.idx_dim;
+  struct Row {
+    uint4 a0, a1, r, k;    // 16 latent dims, 8 RoPE dims, 8 key dims
+    int64_t to;            // row of the cache, or -1
+  };
+  // all loads of a row
+  auto fetch = [&](int64_t row) {
+    Row x;
+    x.a0 = x.a1 = x.r = x.k = make_uint4(0, 0, 0, 0);
+    x.to = -1;
+    const int32_t b = static_cast<int32_t>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.n));
+    const int32_t j = static_cast<int32_t>(row - static_cast<int64_t>(b) * p.n);
     const int32_t s = p.src != nullptr ? __ldg(p.src + row) : j;
     const int64_t pos = (p.start != nullptr ? static_cast<int64_t>(__ldg(p.start + b)) : 0) + j;
-    const int64_t end = p.lengths != nullptr ? static_cast<int64_t>(__ldg(p.lengths + b)) : p.max_len;
-    if (s < 0 || pos < 0 || (p.lengths != nullptr && pos >= end)) continue;
+    if (s < 0 || pos < 0 || (p.lengths != nullptr && pos >= __ldg(p.lengths + b))) return x;
     if (s >= p.n_src || pos >= p.max_len) {
       if (lane == 0) record_error(p.status, DSA_ERR_INDEX_RANGE, static_cast<uint32_t>(row));
-      continue;
+      return x;
     }
-    const int64_t from = b * p.n_src + s, to = b * p.max_len + pos;
-    // every load of the row first
-    uint4 a0 = zero, a1 = zero, r = zero, k = zero;
-    const bool has_lat = p.latent != nullptr && static_cast<int32_t>(16 * lane) < p.d_latent;
-    const bool has_rope = p.latent != nullptr && static_cast<int32_t>(8 * lane) < p.d_rope;
-    const bool has_key = p.keys != nullptr && static_cast<int32_t>(8 * lane) < p.idx_dim;
+    const int64_t from = static_cast<int64_t>(b) * p.n_src + s;
+    x.to = static_cast<int64_t>(b) * p.max_len + pos;
     const __nv_bfloat16* lat = p.latent + from * (p.d_latent + p.d_rope);
     if (has_lat) {
-      const uint4* x = reinterpret_cast<const uint4*>(lat + 16 * lane);
-      a0 = __ldg(x);
-      a1 = __ldg(x + 1);
+      const uint4* src = reinterpret_cast<const uint4*>(lat + 16 * lane);
+      x.a0 = __ldg(src);
+      x.a1 = __ldg(src + 1);
     }
-    if (has_rope) r = __ldg(reinterpret_cast<const uint4*>(lat + p.d_latent + 8 * lane));
-    if (has_key) k = __ldg(reinterpret_cast<const uint4*>(p.keys + from * p.idx_dim + 8 * lane));
+    if (has_rope) x.r = __ldg(reinterpret_cast<const uint4*>(lat + p.d_latent + 8 * lane));
+    if (has_key) x.k = __ldg(reinterpret_cast<const uint4*>(p.keys + from * p.idx_dim + 8 * lane));
+    return x;
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRowWarps;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp_id(); row < p.rows; row += step) {
+    const Row x = fetch(row);
+    if (x.to < 0) continue;
+    // magnitudes as they are; in the rare row with an infinity or a NaN, those left out
+    uint32_t m = max(max4(x.a0, 0x7FFF7FFFu), max4(x.a1, 0x7FFF7FFFu)), mk = max4(x.k, 0x7FFF7FFFu);
+    uint32_t nans = 0;                                     // lanes whose latents hold a NaN
+    if (__any_sync(0xffffffffu, max(m, mk) >= kNonFinite)) {
+      nans = __ballot_sync(0xffffffffu, m > kNonFinite);
+      m = max(max4_finite(x.a0), max4_finite(x.a1));
+      mk = max4_finite(x.k);
+    }
     if (p.latent != nullptr) {
-      // 8 lanes hold a group of 128
-      uint32_t m = __vmaxu2(__vmaxu2(__vmaxu2(finite_mag2(a0.x), finite_mag2(a0.y)),
-                                     __vmaxu2(finite_mag2(a0.z), finite_mag2(a0.w))),
-                            __vmaxu2(__vmaxu2(finite_mag2(a1.x), finite_mag2(a1.y)),
-                                     __vmaxu2(finite_mag2(a1.z), finite_mag2(a1.w))));
-      const bool nan = has_nan2(a0.x) || has_nan2(a0.y) || has_nan2(a0.z) || has_nan2(a0.w) || has_nan2(a1.x) ||
-                       has_nan2(a1.y) || has_nan2(a1.z) || has_nan2(a1.w);
-      const uint32_t nans = __ballot_sync(0xffffffffu, nan);
-      const int e = scale_exp(group_max(max(m & 0xFFFFu, m >> 16), 8));
-      const float inv = pow2f(-e);
+      const int e = scale_exp(group_max<8>(m));            // 8 lanes hold a group of 128
+      const uint64_t inv2 = pack_f32x2(pow2f(-e), pow2f(-e));
       if (has_lat) {
-        reinterpret_cast<uint4*>(p.cache.codes + to * p.d_latent)[lane] =
-            make_uint4(e4m3x4(a0.x, a0.y, inv), e4m3x4(a0.z, a0.w, inv), e4m3x4(a1.x, a1.y, inv),
-                       e4m3x4(a1.z, a1.w, inv));
+        reinterpret_cast<uint4*>(p.cache.codes + x.to * p.d_latent)[lane] =
+            make_uint4(e4m3x4(x.a0.x, x.a0.y, inv2), e4m3x4(x.a0.z, x.a0.w, inv2), e4m3x4(x.a1.x, x.a1.y, inv2),
+                       e4m3x4(x.a1.z, x.a1.w, inv2));
         if ((lane & 7u) == 0)
-          p.cache.scales[to * groups + (lane >> 3)] = ((nans >> lane) & 0xFFu) ? __int_as_float(0x7FC00000) : pow2f(e);
+          p.cache.scales[x.to * groups + (lane >> 3)] = ((nans >> lane) & 0xFFu) ? __int_as_float(0x7FC00000) : pow2f(e);
       }
-      if (has_rope) reinterpret_cast<uint4*>(p.cache.rope + to * p.d_rope)[lane] = r;
+      if (has_rope) reinterpret_cast<uint4*>(p.cache.rope + x.to * p.d_rope)[lane] = x.r;
     }
     if (p.keys != nullptr) {
-      // 16 lanes hold the key (idx_dim <= 128)
-      const uint32_t m = __vmaxu2(__vmaxu2(finite_mag2(k.x), finite_mag2(k.y)),
-                                  __vmaxu2(finite_mag2(k.z), finite_mag2(k.w)));
-      const int e = scale_exp(group_max(max(m & 0xFFFFu, m >> 16), 16));
-      const float inv = pow2f(-e);
+      const int e = scale_exp(group_max<16>(mk));          // 16 lanes hold the key (idx_dim <= 128)
+      const uint64_t inv2 = pack_f32x2(pow2f(-e), pow2f(-e));
       if (has_key)
-        reinterpret_cast<uint2*>(p.k_idx + to * p.idx_dim)[lane] =
-            make_uint2(e4m3x4(k.x, k.y, inv), e4m3x4(k.z, k.w, inv));
-      if (lane == 0) p.k_scale[to] = pow2f(e);
+        reinterpret_cast<uint2*>(p.k_idx + x.to * p.idx_dim)[lane] =
+            make_uint2(e4m3x4(x.k.x, x.k.y, inv2), e4m3x4(x.k.z, x.k.w, inv2));
+      if (lane == 0) p.k_scale[x.to] = pow2f(e);
     }
   }
 }
@@ -199,13 +223,13 @@ struct QCacheReadParams {
   int64_t rows;                  // B * n
 };
 
-__global__ void __launch_bounds__(kRowThreads) qcache_read_kernel(const QCacheReadParams p) {
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) qcache_read_kernel(const QCacheReadParams p) {
   const uint32_t lane = lane_id();
   const int groups = (p.d_latent + kScaleGroup - 1) / kScaleGroup;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + warp_id(); row < p.rows;
        row += static_cast<int64_t>(gridDim.x) * kRowWarps) {
-    const int64_t b = row / p.n;
+    const int64_t b = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.n);
     int64_t pos;
     bool ok;
     if (p.listed != nullptr) {
