@@ -11,6 +11,7 @@ allocate outputs for convenience.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -98,7 +99,8 @@ def dsa_status_string(status: int) -> str:
 
 
 def dsa_set_wait_budget_ns(ns: int):
-    """Test setting: budget of the indexer's pipeline waits in ns (0 = the default 2 s)."""
+    """Test setting: budget of the pipeline waits of the indexer and of the attention over an 8-bit cache or a
+    drafted tree, in ns (0 = the default 2 s)."""
     _check(_lib.dsa_set_wait_budget_ns(int(ns)), "dsa_set_wait_budget_ns")
 
 
@@ -382,12 +384,22 @@ class QCache:
                       torch.zeros((b, n, dims.idx_dim), dtype=torch.uint8, device=device),
                       torch.ones((b, n), dtype=torch.float32, device=device))
 
-    def _struct(self, dims: dsa_dims, device) -> dsa_qcache:
+    def _struct(self, dims: dsa_dims, device: int) -> dsa_qcache:
         rows = dims.batch * dims.max_len
         _same("cache.codes", self.codes, torch.uint8, rows * dims.d_latent, device)
         _same("cache.scales", self.scales, torch.float32, rows * -(-dims.d_latent // _SCALE_GROUP), device)
         _same("cache.rope", self.rope, torch.bfloat16, rows * dims.d_rope, device)
         return dsa_qcache(_ptr(self.codes), _ptr(self.scales), _ptr(self.rope))
+
+
+def _allocating(stream):
+    """Outputs of a call on ``stream`` come from that stream's memory: memory of the current stream could still
+    be in use there by earlier work that the call does not wait for."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 def _per_sequence(dims, device, **tensors):
@@ -431,24 +443,26 @@ def qcache_read(dims, cache: QCache, ws: Workspace, rows=None, start=None, lengt
     if rows is not None:
         _same("rows", rows, torch.int32, dims.batch * dims.n_q, device)
     _per_sequence(dims, device, start=start, lengths=lengths)
-    out = cache.rope.new_empty((dims.batch, dims.n_q, dims.d_latent + dims.d_rope))
+    with _allocating(stream):
+        out = cache.rope.new_empty((dims.batch, dims.n_q, dims.d_latent + dims.d_rope))
     dsa_qcache_read(dims, cache._struct(dims, device), rows, start, lengths, out, ws.buf, stream)
     return out
 
 
-def _attention_inputs(dims, q, idx, topk, ws):
+def _attention_inputs(dims, q, idx, topk, stream):
     device = _call_device(q)
     queries = dims.batch * dims.n_q
     _same("q", q, torch.bfloat16, queries * dims.n_heads * (dims.d_latent + dims.d_rope), device)
     _same("idx", idx, torch.int32, queries * topk, device)
-    out = q.new_empty((dims.batch, dims.n_q, dims.n_heads, dims.d_latent))
-    lse = q.new_empty((dims.batch, dims.n_q, dims.n_heads), dtype=torch.float32)
+    with _allocating(stream):
+        out = q.new_empty((dims.batch, dims.n_q, dims.n_heads, dims.d_latent))
+        lse = q.new_empty((dims.batch, dims.n_q, dims.n_heads), dtype=torch.float32)
     return device, out, lse
 
 
 def sparse_mla_attn_qcache(dims, q, cache: QCache, idx, topk, ws: Workspace, stream=None):
     """``sparse_mla_attn`` over an 8-bit cache. Returns (out bf16 [B, n_q, H, d_latent], lse fp32 [B, n_q, H])."""
-    device, out, lse = _attention_inputs(dims, q, idx, topk, ws)
+    device, out, lse = _attention_inputs(dims, q, idx, topk, stream)
     dsa_sparse_mla_attn_qcache(dims, q, cache._struct(dims, device), idx, topk, out, lse, ws.buf, stream)
     return out, lse
 
@@ -458,7 +472,7 @@ def tree_mla_attn(dims, q, cache, idx, topk, draft, parents, ws: Workspace, stre
     to the drafted rows on its path. ``cache`` is a ``QCache`` or a bf16 latent cache [B, max_len, d]; ``draft``
     bf16 [B, n_q, d]; ``parents`` int32 [B, n_q] (-1: child of the last committed token, < -1: absent node).
     Returns (out, lse) like ``sparse_mla_attn``."""
-    device, out, lse = _attention_inputs(dims, q, idx, topk, ws)
+    device, out, lse = _attention_inputs(dims, q, idx, topk, stream)
     width = dims.d_latent + dims.d_rope
     _same("draft", draft, torch.bfloat16, dims.batch * dims.n_q * width, device)
     _same("parents", parents, torch.int32, dims.batch * dims.n_q, device)

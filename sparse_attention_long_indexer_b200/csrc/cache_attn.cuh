@@ -165,7 +165,8 @@ struct ClockWaiter {
   volatile int* abort;
   int64_t budget;            // clocks
   __device__ __forceinline__ bool aborted() const { return *abort != 0; }
-  // One more unsuccessful try: false once the CTA has aborted or the budget is spent.
+  // One more unsuccessful try: false once the CTA has aborted or the budget is spent (looked at every 64th
+  // time).
   __device__ __forceinline__ bool again(uint32_t& spins, int64_t& t0, uint32_t tag) const {
     if ((++spins & 63u) != 0) return true;
     if (*abort) return false;
@@ -184,8 +185,15 @@ struct ClockWaiter {
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t tag) const {
     uint32_t spins = 0;
     int64_t t0 = 0;
-    while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))
+    while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+      // a try may suspend the thread for longer than this kernel's waits: with a budget under 1 us (a test's
+      // setting) the first unsuccessful one is the last
+      if (budget < 2000) {
+        spins = 63;
+        t0 = 1;
+      }
       if (!again(spins, t0, tag)) return false;
+    }
     return true;
   }
   // The low half of the 64-bit shared word at `addr` once its high half is `number` (one aligned store

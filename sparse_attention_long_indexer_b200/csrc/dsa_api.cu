@@ -90,7 +90,8 @@ struct NvtxRange {
 };
 
 constexpr uint64_t kWaitBudgetNs = 2000000000ull;   // 2 s per bounded wait
-// budget of the indexer's pipeline waits (dsa_set_wait_budget_ns, a test setting)
+// budget of the pipeline waits of the indexer and of the attention over caches (dsa_set_wait_budget_ns, a
+// test setting)
 std::atomic<uint64_t> g_indexer_wait_ns{kWaitBudgetNs};
 constexpr size_t kAlign = 256;
 constexpr int kPrefillNQ = 4;                       // queries per prefill indexer work item
@@ -699,7 +700,7 @@ const char* dsa_status_string(dsa_status status) {
   return "unknown status";
 }
 
-int32_t dsa_version(void) { return 200; }
+int32_t dsa_version(void) { return 300; }
 
 dsa_status dsa_set_wait_budget_ns(uint64_t ns) {
   g_indexer_wait_ns.store(ns == 0 ? kWaitBudgetNs : ns, std::memory_order_relaxed);
@@ -934,7 +935,7 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   p.split_blocks = plan.split_blocks;
   p.n_items = static_cast<int32_t>(queries * plan.n_splits);
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
-  p.wait_budget_ns = kWaitBudgetNs;
+  p.wait_budget_ns = g_indexer_wait_ns.load(std::memory_order_relaxed);
   CUtensorMap map_q;
   if (!encode_q_rows(&map_q, q, static_cast<uint64_t>(queries) * d.n_heads,
                      static_cast<uint64_t>(d.d_latent + d.d_rope)))

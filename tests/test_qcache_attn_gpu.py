@@ -264,7 +264,108 @@ def test_absent_nodes_invalid_parents_and_rows_off_the_path():
     assert torch.equal(out3[1], out[1])
 
 
+@pytest.mark.parametrize("d_latent,d_rope,heads", [(24, 8, 3), (248, 64, 65), (504, 0, 128), (8, 24, 1), (512, 56, 64)])
+def test_trees_over_a_bf16_cache_of_odd_dims(d_latent, d_rope, heads):
+    dims = dsa.make_dims(2, 5, 90, n_heads=heads, d_latent=d_latent, d_rope=d_rope)
+    g = torch.Generator().manual_seed(40)
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16)             # noqa: E731
+    q, kv, draft = rnd(2, 5, heads, d_latent + d_rope), rnd(2, 90, d_latent + d_rope).cuda(), rnd(2, 5, d_latent + d_rope)
+    parents, idx = _parents(41, 2, 5), _lists(42, 2, 5, 70, 90)
+    ws = dsa.Workspace.create_qcache(dims, 70)
+    out, lse = dsa.tree_mla_attn(dims, q.cuda(), kv, idx.cuda(), 70, draft.cuda(), parents.cuda(), ws)
+    ws.check()
+    _check_all(dims, out, lse, q, lambda b, i: _tree_rows(kv, b, idx[b, i], draft, parents, i, 90))
+
+
+@pytest.mark.parametrize("d_latent,d_rope,heads", [(16, 8, 2), (128, 64, 128), (240, 40, 65), (256, 64, 64),
+                                                   (272, 8, 100), (496, 64, 127), (512, 0, 128)])
+def test_listed_rows_of_odd_dims(d_latent, d_rope, heads):
+    dims = dsa.make_dims(1, 6, 200, n_heads=heads, d_latent=d_latent, d_rope=d_rope)
+    g = torch.Generator().manual_seed(43)
+    cache = dsa.QCache.create(dims)
+    codes = (torch.randn(cache.codes.shape, generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
+    cache.codes.copy_(codes.view(torch.uint8))
+    cache.scales.copy_(torch.exp2(torch.randint(-9, -5, cache.scales.shape, generator=g).float()))
+    cache.rope.copy_(torch.randn(cache.rope.shape, generator=g).to(torch.bfloat16))
+    q = torch.randn((1, 6, heads, d_latent + d_rope), generator=g).to(torch.bfloat16)
+    idx = _lists(44, 1, 6, 150, 200)
+    ws = dsa.Workspace.create_qcache(dims, 150)
+    out, lse = dsa.sparse_mla_attn_qcache(dims, q.cuda(), cache, idx.cuda(), 150, ws)
+    ws.check()
+    _check_all(dims, out, lse, q, lambda b, i: _listed_rows(cache, b, idx[b, i], 200))
+
+
+def test_codes_and_scales_of_another_writer():
+    # E4M3's NaN codes read as NaN; a scale need not be a power of two
+    dims, cache, q, ws = _setup("prod", 1, 3, 70, 70, seed=45)
+    cache.scales.mul_(1.25)
+    cache.codes[0, 9, 100] = 0x7F
+    idx = torch.arange(70, dtype=torch.int32).expand(1, 3, 70).clone()
+    idx[0, 0, 9] = idx[0, 2, 9] = -1
+    out, lse = dsa.sparse_mla_attn_qcache(dims, q.cuda(), cache, idx.cuda(), 70, ws)
+    ws.check()
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1]).all()
+    back = dsa.qcache_read(dsa.make_dims(1, 70, 70, **DIMS["prod"]), cache, ws).cpu().double()[0]
+    assert torch.isnan(back[9, 100]) and torch.isfinite(back[9, :100]).all()
+    for i in (0, 2):                                   # the rows as read back: code * scale rounded to bf16
+        check(out[0, i], lse[0, i], attend(q[0, i].double(), back[idx[0, i][idx[0, i] >= 0].long()], 512,
+                                           dims.softmax_scale))
+
+
+def test_many_items_of_every_length_one_after_another():
+    # more queries than pairs of SMs, ranges from none to several blocks, so that consecutive items of a pair
+    # meet every combination of ring stage and buffer
+    n = 700
+    dims, cache, q, ws = _setup("prod", 1, n, 800, 330, seed=46)
+    r = np.random.default_rng(47)
+    idx = np.full((1, n, 330), -1, dtype=np.int32)
+    for i in range(n):
+        k = int(r.integers(0, 331)) if i % 7 else 0
+        idx[0, i, :k] = r.integers(0, 800, k)
+    idx = torch.from_numpy(idx)
+    first = None
+    for _ in range(3):
+        out, lse = dsa.sparse_mla_attn_qcache(dims, q.cuda(), cache, idx.cuda(), 330, ws)
+        ws.check()
+        if first is None:
+            first = (out.clone(), lse.clone())
+            _check_all(dims, out, lse, q, lambda b, i: _listed_rows(cache, b, idx[b, i], 800), range(0, n, 9))
+        else:                                          # no atomics: the same bits every time
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
 # ----------------------------------------------------------------------------- streams, graphs, both together
+def test_a_call_on_a_given_stream():
+    dims, cache, q, ws = _setup("prod", 1, 2, 500, 300, seed=48)
+    idx = _lists(49, 1, 2, 300, 500).cuda()
+    q = q.cuda()
+    want = dsa.sparse_mla_attn_qcache(dims, q, cache, idx, 300, ws)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        out, lse = dsa.sparse_mla_attn_qcache(dims, q, cache, idx, 300, ws, stream=s)
+        side.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    ws.check()
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean():
+    for n, topk in ((2, 1024), (300, 130)):            # ranges with a join, and many items
+        dims, cache, q, ws = _setup("prod", 1, n, 2000, topk, seed=50)
+        idx = _lists(51, 1, n, topk, 2000)
+        dsa.dsa_set_wait_budget_ns(1)
+        try:
+            dsa.sparse_mla_attn_qcache(dims, q.cuda(), cache, idx.cuda(), topk, ws)
+            torch.cuda.synchronize()
+            status, detail = dsa.dsa_get_device_status(ws.buf)
+        finally:
+            dsa.dsa_set_wait_budget_ns(0)
+        assert status == dsa.DSA_ERR_DEVICE_TIMEOUT and detail >> 16 == 4
+        out, lse = dsa.sparse_mla_attn_qcache(dims, q.cuda(), cache, idx.cuda(), topk, ws)
+        ws.check()
+        _check_all(dims, out, lse, q, lambda b, i: _listed_rows(cache, b, idx[b, i], 2000), [0, 1, n - 1])
+
+
 def test_other_streams_and_replayed_graphs():
     cases = []
     for seed in (20, 21):                              # two captured graphs with a workspace each
