@@ -18,7 +18,7 @@
 // which needs no cluster but computes and expands everything for the logits twice, took 1.67 ms for
 // 1024 queries of 2048 rows.)
 //
-// One CTA, 23 warps:
+// One CTA, 24 warps:
 //  * control (1 warp): how far the range's list reaches, a node's path, and the item's q, ahead of the item.
 //  * producers: 8 warps bring this CTA's 32 rows of each block, all dims (the logits' operand), 8 warps
 //    all 64 rows' dims that it supplies to the output; each part has a 2-stage ring of
@@ -27,7 +27,8 @@
 //    on purpose: the L1 keeps 60 KB, which is what loads in flight land in. bf16 rows (drafted rows,
 //    bf16 cache) are copied with cp.async. Rows that are not attended (padding, out of range, off
 //    the path) are zero rows, so nothing they hold in memory reaches a product.
-//  * MMA: one warp issues the logits, one the outputs (even CTA).
+//  * MMA: one warp issues the logits, one the outputs (even CTA); in the odd CTA they, and one more, pass on
+//    what its own warps have ready.
 //  * softmax: 4 warps; lane L has rows 32 (L / 64) .. +31 of a block of head L % 64 of this CTA.
 //    Online softmax in the log2 domain; the running max is raised, and the output rescaled, only when
 //    it grows by more than kLazyRescale.
@@ -62,7 +63,8 @@ struct CacheAttnCfg {
   static constexpr int S_WARP = SOFTMAX_WARPS + PRODUCER_WARPS;   // logits MMAs (and TMEM owner)
   static constexpr int O_WARP = S_WARP + 1;                       // output MMAs
   static constexpr int CTRL_WARP = S_WARP + 2;
-  static constexpr int THREADS = (CTRL_WARP + 1) * 32;
+  static constexpr int R_WARP = S_WARP + 3;                       // odd CTA: one of its three relays
+  static constexpr int THREADS = (R_WARP + 1) * 32;
   // TMEM columns
   static constexpr uint32_t COL_O = 0, COL_S = 256, COL_Q = COL_S + 32 * S_BUFS, TMEM_COLS = 512;
   // shared memory
@@ -74,7 +76,7 @@ struct CacheAttnCfg {
   static constexpr int OFF_INFO = OFF_XCHG + 2 * 128 * 8;
   static constexpr int INFO_WORDS = 4 + kMaxDraft / 32;  // list blocks, drafted blocks, first drafted block, -, path
   static constexpr int OFF_BAR = OFF_INFO + 2 * INFO_WORDS * 4;
-  static constexpr int NUM_BARS = 28;
+  static constexpr int NUM_BARS = 32;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
   static_assert(OFF_O % 1024 == 0 && OFF_QS % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "layout");
@@ -230,9 +232,11 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   const uint32_t q_empty = B(10);                            // commit: the item's logits are done
   const uint32_t q_tma = B(11);                              // this CTA's q has landed in shared memory
   auto p_local = [&](uint32_t j) { return B(12 + j); };      // odd CTA's softmax warps: P written
+  auto l_local = [&](uint32_t s) { return B(28 + s); };      // odd CTA's producer warps: its logits part is in
+  auto v_local = [&](uint32_t s) { return B(30 + s); };      // the same for its output part
   // in the even CTA, arrived on by both
-  auto l_full = [&](uint32_t s) { return B(14 + s); };       // producer warps: a logits part is in
-  auto v_full = [&](uint32_t s) { return B(16 + s); };       // producer warps: an output part is in
+  auto l_full = [&](uint32_t s) { return B(14 + s); };       // its producer warps, a relay: a logits part is in
+  auto v_full = [&](uint32_t s) { return B(16 + s); };       // its producer warps, a relay: an output part is in
   const uint32_t q_full = B(18);                             // producer warps: q is in (TMEM and shared memory)
   auto p_full = [&](uint32_t j) { return B(19 + j); };       // its softmax warps, and the odd CTA's relay
   const uint32_t o_empty = B(21);                            // softmax warps: outputs read
@@ -253,12 +257,14 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(info_full(i), 1);
-      // softmax and producer warps, and the MMA warps (odd CTA: the relay)
-      mbar_init(info_empty(i), C::SOFTMAX_WARPS + C::PRODUCER_WARPS + (leader ? 2 : 1));
+      // softmax and producer warps, and the MMA warps (odd CTA: the relays)
+      mbar_init(info_empty(i), C::SOFTMAX_WARPS + C::PRODUCER_WARPS + (leader ? 2 : 3));
       mbar_init(o_done(i), 1);
       mbar_init(p_local(i), C::SOFTMAX_WARPS);
-      mbar_init(l_full(i), 2 * C::PART_WARPS);
-      mbar_init(v_full(i), 2 * C::PART_WARPS);
+      mbar_init(l_full(i), C::PART_WARPS + 1);
+      mbar_init(v_full(i), C::PART_WARPS + 1);
+      mbar_init(l_local(i), C::PART_WARPS);
+      mbar_init(v_local(i), C::PART_WARPS);
       mbar_init(p_full(i), C::SOFTMAX_WARPS + 1);
     }
     for (uint32_t i = 0; i < static_cast<uint32_t>(C::S_BUFS); ++i) {
@@ -450,7 +456,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       auto announce = [&]() {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_leader(logits_part ? l_full(nb & 1u) : v_full(nb & 1u));
+        const uint32_t st = nb & 1u;
+        if (lane == 0) mbar_arrive(leader ? (logits_part ? l_full(st) : v_full(st)) : (logits_part ? l_local(st) : v_local(st)));
       };
       // one block of bf16 rows: row r of a table, zeros where r < 0
       auto copy_block = [&](const __nv_bfloat16* table, int32_t r) -> bool {
@@ -657,7 +664,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     // after an abort the q copy in flight lands before the CTA may leave (else it has landed)
     if (lane == 0 && n_busy > 0 && wt.aborted()) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
   } else if (warp >= static_cast<uint32_t>(C::S_WARP)) {
-    // ================================================================ MMA issuers (even CTA), relay (odd CTA)
+    // ================================================================ MMA issuers (even CTA), relays (odd CTA)
     // One warp issues the logits MMAs, one the output MMAs, so that each one's waits (issue blocks
     // while the pipe is full) overlap the other's work. A commit tracks the MMAs of its own thread.
     constexpr uint32_t idesc_s = make_idesc(1, 1, 0, 0, 128, C::BLK);
@@ -666,7 +673,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     const int32_t out_instr = p.d_latent > 256 ? 2 : 1;
     uint32_t n_it = 0, n_busy = 0, nb = 0;
     uint32_t buf = 0, buf_par = 0;                       // logits buffer, and the parity of its use
-    bool ok = leader || logits;                          // the odd CTA's second warp has nothing to do
+    bool ok = !leader || warp != static_cast<uint32_t>(C::R_WARP);      // which has nothing to do in the even CTA
     for (int32_t it = pair; it < p.n_items && ok; it += n_pairs, ++n_it) {
       const uint32_t slot = n_it & 1u, sph = (n_it >> 1) & 1u;
       if (!warp_wait(info_full(slot), sph, 10)) break;
@@ -675,11 +682,16 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       if (lane == 0) mbar_arrive(info_empty(slot));
       if (n_blocks == 0) continue;
       if (!leader) {
-        // relay: the odd CTA's softmax warps announce P locally (a CTA-scope arrive does not stall
-        // them); one cluster-scope arrive, which by cumulativity carries the observed P stores, follows
+        // Relays, one each for P, the logits part and the output part: the odd CTA's warps announce theirs
+        // locally, and one cluster-scope arrive, which by cumulativity carries the observed stores, follows.
+        // From a producer warp that arrive took 1.5K clocks of every block (a CTA-scope one 0.4K).
+        const bool l_part = warp == static_cast<uint32_t>(C::O_WARP);
+        const uint32_t from = logits ? p_local(0) : l_part ? l_local(0) : v_local(0);
+        const uint32_t to = lead_off + (logits ? p_full(0) : l_part ? l_full(0) : v_full(0));
         for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
-          if (!warp_wait(p_local(nb & 1u), (nb >> 1) & 1u, 11)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_cluster(p_full(nb & 1u) + lead_off);
+          const uint32_t st = nb & 1u;
+          if (!warp_wait(from + 8u * st, (nb >> 1) & 1u, 11)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_cluster(to + 8u * st);
           __syncwarp();
         }
       } else if (logits) {
@@ -743,7 +755,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       }
       ++n_busy;
     }
-    if (leader && elect_one()) {
+    if (leader && warp != static_cast<uint32_t>(C::R_WARP) && elect_one()) {
       commit2(mma_done);
       attn_drain_wait(mma_done, 0, kDrainBudgetNs);
     }
