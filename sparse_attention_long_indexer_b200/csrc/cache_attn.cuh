@@ -930,60 +930,86 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       ++n_busy;
       tc_fence_after();
       const float inv = l_r == 0.f ? 0.f : 1.0f / l_r;
-      // 32 dims of 32 heads at a time go through this warp's 4 KB of the P buffers (free now: the outputs
-      // that read them are done), so that a store instruction writes whole 128-byte (fp32) or 64-byte
-      // (bf16) pieces of rows; straight from the lanes, a row each, it took 10K clocks. The 16-byte chunks
-      // are swizzled so that eight lanes at a time, writing or reading, fall into distinct bank groups.
+      // 128 bytes of 32 heads (64 dims in bf16, 32 in fp32) at a time go through this warp's 4 KB of the P buffers
+      // (free now: the outputs that read them are done), so that a store instruction writes whole 128-byte
+      // pieces of rows; straight from the lanes, a row each, it took 10K clocks. The 16-byte chunks are
+      // swizzled so that eight lanes at a time, writing or reading, fall into distinct bank groups.
       const uint32_t tile = sbase + C::OFF_P + warp * 4096u;
       const int32_t head0 = static_cast<int32_t>(64u * rank + (warp & 1u) * 32u);       // of lane 0
-#pragma unroll 1
-      for (int k = 0; k < 8; ++k) {                      // 2 instructions x 128 columns, 32 at a time
-        const int32_t dim = 256 * (k >> 2) + 128 * static_cast<int32_t>(part) + 32 * (k & 3);
-        if (dim >= p.d_latent) break;                    // (rises with k)
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_off + C::COL_O + 32 * k, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * inv);
+      const uint32_t ch = lane & 7u;
+      // lane's row in, chunk `ch` of rows lane / 8, + 4, ... out
+      auto turn = [&](const uint32_t (&w)[32]) {
         __syncwarp();                                    // the previous pass has been read
-        if (p.n_splits == 1) {
-          const uint32_t at = tile + (lane >> 1) * 128u;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
+        for (int u = 0; u < 8; ++u)
+          st_shared_v4(tile + lane * 128u + ((u ^ (lane & 7u)) << 4), make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
+        __syncwarp();
+      };
+      // rows 16 half + 4 i + lane / 8
+      auto fetch4 = [&](int half, uint4 (&x)[4]) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t r = 16u * half + 4u * i + (lane >> 3);
+          x[i] = ld_shared_v4(tile + r * 128u + ((ch ^ (r & 7u)) << 4));
+        }
+      };
+      // dims of column group k of `width` columns (2 instructions x 128 columns)
+      auto dim_of = [&](int k, int width) {
+        const int32_t col = k * width;
+        return 256 * (col >> 7) + 128 * static_cast<int32_t>(part) + (col & 127);
+      };
+      const int32_t heads = p.n_heads - head0 - static_cast<int32_t>(lane >> 3);        // this lane's rows 4 i < heads are heads
+      if (p.n_splits == 1) {
+        __nv_bfloat16* base = p.out + (static_cast<size_t>(m.qi) * p.n_heads + head0 + (lane >> 3)) * p.d_latent + 8 * ch;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const int32_t dim = dim_of(k, 64);
+          if (dim >= p.d_latent) break;                  // (rises with k)
+          uint32_t w[32];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + C::COL_O + 64 * k + 32 * h, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
               const __nv_bfloat162 pr =
-                  __floats2bfloat162_rn(__uint_as_float(o[8 * u + 2 * x]), __uint_as_float(o[8 * u + 2 * x + 1]));
-              w[x] = *reinterpret_cast<const uint32_t*>(&pr);
+                  __floats2bfloat162_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
+              w[16 * h + u] = *reinterpret_cast<const uint32_t*>(&pr);
             }
-            st_shared_v4(at + ((((lane & 1u) * 4u + u) ^ ((lane >> 1) & 7u)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
           }
-          __syncwarp();
-          const uint32_t ch = lane & 3u;
+          turn(w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t r = 8u * i + (lane >> 2);
-            const uint4 x = ld_shared_v4(tile + (r >> 1) * 128u + ((((r & 1u) * 4u + ch) ^ ((r >> 1) & 7u)) << 4));
-            const int32_t hd = head0 + static_cast<int32_t>(r), d = dim + 8 * static_cast<int32_t>(ch);
-            if (hd < p.n_heads && d < p.d_latent)
-              *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(m.qi) * p.n_heads + hd) * p.d_latent + d) = x;
+          for (int half = 0; half < 2; ++half) {
+            uint4 x[4];
+            fetch4(half, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * half + 4 * i < heads && dim + 8 * static_cast<int32_t>(ch) < p.d_latent)
+                *reinterpret_cast<uint4*>(base + static_cast<size_t>(16 * half + 4 * i) * p.d_latent + dim) = x[i];
           }
-        } else {
-          const uint32_t at = tile + lane * 128u;
+        }
+      } else {
+        float* base = p.part_out + ((static_cast<size_t>(m.qi) * p.n_splits + m.split) * p.n_heads + head0 + (lane >> 3)) *
+                                       p.d_latent + 4 * ch;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const int32_t dim = dim_of(k, 32);
+          if (dim >= p.d_latent) break;
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + C::COL_O + 32 * k, o);
+          tmem_wait_ld();
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            st_shared_v4(at + ((u ^ (lane & 7u)) << 4), make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
-          __syncwarp();
-          const uint32_t ch = lane & 7u;
-          float* base = p.part_out + (static_cast<size_t>(m.qi) * p.n_splits + m.split) * p.n_heads * p.d_latent;
+          for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * inv);
+          turn(o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t r = 4u * i + (lane >> 3);
-            const uint4 x = ld_shared_v4(tile + r * 128u + ((ch ^ (r & 7u)) << 4));
-            const int32_t hd = head0 + static_cast<int32_t>(r), d = dim + 4 * static_cast<int32_t>(ch);
-            if (hd < p.n_heads && d < p.d_latent)
-              *reinterpret_cast<uint4*>(base + static_cast<size_t>(hd) * p.d_latent + d) = x;
+          for (int half = 0; half < 2; ++half) {
+            uint4 x[4];
+            fetch4(half, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * half + 4 * i < heads && dim + 4 * static_cast<int32_t>(ch) < p.d_latent)
+                *reinterpret_cast<uint4*>(base + static_cast<size_t>(16 * half + 4 * i) * p.d_latent + dim) = x[i];
           }
         }
       }
