@@ -141,24 +141,27 @@ __device__ __forceinline__ void st_shared_v4(uint32_t dst, const uint4& v) {
 }
 
 // Loads that stay where they are written (volatile): the producers issue a block's loads one block
-// before their use, and a load that the compiler may move is moved down to its use. Zero without `in`.
-__device__ __forceinline__ uint4 ld_ahead_v4(const void* src, bool in) {
+// before their use, and a load that the compiler may move is moved down to its use. Piece kPiece of
+// the n that there are, kOff bytes on; zero where there are fewer.
+template <int kPiece, int kOff>
+__device__ __forceinline__ uint4 ld_ahead_v4(const void* src, int32_t n) {
   uint4 v;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %5, %6;\n\t"
       "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4 + %7];\n\t}"
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(src), "r"(static_cast<uint32_t>(in)));
+      : "l"(src), "r"(n), "n"(kPiece), "n"(kOff));
   return v;
 }
-__device__ __forceinline__ float ld_ahead_f32(const float* src, bool in) {
+template <int kPiece, int kOff>
+__device__ __forceinline__ float ld_ahead_f32(const float* src, int32_t n) {
   float v;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0f00000000;\n\t"
-      "@p ld.global.nc.f32 %0, [%1];\n\t}"
+      "{\n\t.reg .pred p;\n\tsetp.gt.s32 p, %2, %3;\n\tmov.b32 %0, 0f00000000;\n\t"
+      "@p ld.global.nc.f32 %0, [%1 + %4];\n\t}"
       : "=&f"(v)
-      : "l"(src), "r"(static_cast<uint32_t>(in)));
+      : "l"(src), "r"(n), "n"(kPiece), "n"(kOff));
   return v;
 }
 
@@ -363,17 +366,16 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     const uint32_t row = logits_part ? 4u * (gt >> 5) + 2u * (lane >> 4) + ((lane >> 2) & 1u) : gt >> 2;   // of the tile
     const uint32_t c = logits_part ? (lane & 3u) + 4u * ((lane >> 3) & 1u) : lane & 3u;
     const uint32_t row_at = (row >> 3) * 1024u + (row & 7u) * 128u;
-    const uint32_t at0 = row_at + (((2 * (c & 3u)) ^ (row & 7u)) << 4);
-    const uint32_t at1 = row_at + (((2 * (c & 3u) + 1) ^ (row & 7u)) << 4);
+    static_assert(2 * C::L_ATOM == C::O_ATOM, "one step from piece to piece");
+    const uint32_t tile_at = row_at + (c >> 2) * C::L_ATOM;
+    const uint32_t at0 = tile_at + (((2 * (c & 3u)) ^ (row & 7u)) << 4);
+    const uint32_t at1 = tile_at + (((2 * (c & 3u) + 1) ^ (row & 7u)) << 4);
     const int32_t block_row = static_cast<int32_t>(row + (logits_part ? 32u * rank : 0u));   // row of the block
-    // piece k of this thread: its first dim, and where it goes in the tile
-    auto piece_dim = [&](int32_t k) -> int32_t {
-      return logits_part ? 16 * (static_cast<int32_t>(c) + 8 * k)
-                         : 256 * (k >> 1) + 128 * static_cast<int32_t>(rank) + 64 * (k & 1) + 16 * static_cast<int32_t>(c);
-    };
-    auto piece_at = [&](int32_t k) -> uint32_t {
-      return logits_part ? (2u * k + (c >> 2)) * C::L_ATOM : static_cast<uint32_t>(k) * C::O_ATOM;
-    };
+    // piece k of this thread: its first dim, and where it goes in the tile, from at0 and at1
+    const int32_t dim0 = 16 * static_cast<int32_t>(c) + (logits_part ? 0 : 128 * static_cast<int32_t>(rank));
+    const int32_t dim_step = logits_part ? 128 : 64;
+    auto piece_dim = [&](int32_t k) -> int32_t { return dim0 + 256 * (k >> 1) + dim_step * (k & 1); };
+    auto piece_at = [](int32_t k) -> uint32_t { return static_cast<uint32_t>(k) * C::O_ATOM; };
     uint32_t n_it = 0, n_busy = 0, nb = 0;                   // items, items with blocks, blocks so far
     uint32_t s_buf = 0, s_par = 0;                           // logits buffer of block nb - 2, and its use's parity
     for (int32_t it = pair; it < p.n_items; it += n_pairs, ++n_it) {
@@ -496,22 +498,33 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         const int32_t rope_k = (p.d_latent / 16 - static_cast<int32_t>(c) + 7) / 8;
         const int32_t rope_d = piece_dim(rope_k) - p.d_latent;
         const bool has_rope = logits_part && rope_d < p.d_rope;
+        int32_t n_codes = 0;                               // pieces of codes that this thread has
+#pragma unroll
+        for (int k = 0; k < 4; ++k) n_codes += piece_dim(k) < p.d_latent ? 1 : 0;
+        const int32_t n_rope = has_rope ? (rope_d + 8 < p.d_rope ? 2 : 1) : 0;
+        // Scales: the logits part's pieces are of one group each, the output part's pieces 2 i and 2 i + 1
+        // of the same one.
+        const int32_t n_odd = logits_part ? 4 : 0;
+        const int32_t group0 = dim0 / kScaleGroup;
         uint4 raw[4], rp[2];
         float sc[4];
         auto load = [&](int32_t r) {
-          const uint8_t* src = codes + static_cast<int64_t>(r) * p.d_latent;
-          const float* s0 = scales + static_cast<int64_t>(r) * groups;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int32_t d = piece_dim(k);
-            const bool in = r >= 0 && d < p.d_latent;
-            raw[k] = ld_ahead_v4(src + d, in);
-            sc[k] = ld_ahead_f32(s0 + d / kScaleGroup, in);
-          }
+          const int32_t n = r >= 0 ? n_codes : 0, odd = min(n, n_odd), nr = r >= 0 ? n_rope : 0;
+          const uint8_t* src = codes + static_cast<int64_t>(r) * p.d_latent + dim0;
+          const uint8_t* src1 = src + dim_step;
+          const float* s0 = scales + static_cast<int64_t>(r) * groups + group0;
+          raw[0] = ld_ahead_v4<0, 0>(src, n);
+          sc[0] = ld_ahead_f32<0, 0>(s0, n);
+          raw[1] = ld_ahead_v4<1, 0>(src1, n);
+          sc[1] = ld_ahead_f32<1, 4>(s0, odd);
+          raw[2] = ld_ahead_v4<2, 256>(src, n);
+          sc[2] = ld_ahead_f32<2, 8>(s0, n);
+          raw[3] = ld_ahead_v4<3, 256>(src1, n);
+          sc[3] = ld_ahead_f32<3, 12>(s0, odd);
           if (has_rope) {
             const __nv_bfloat16* rs = rope + static_cast<int64_t>(r) * p.d_rope + rope_d;
-            rp[0] = ld_ahead_v4(rs, r >= 0);
-            rp[1] = ld_ahead_v4(rs + 8, r >= 0 && rope_d + 8 < p.d_rope);
+            rp[0] = ld_ahead_v4<0, 0>(rs, nr);
+            rp[1] = ld_ahead_v4<1, 16>(rs, nr);
           }
         };
         load(checked(v0));
@@ -525,9 +538,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
           if (!acquire(tile)) { ok = false; break; }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (piece_dim(k) >= p.d_latent) break;
+            if (k >= n_codes) break;
             uint4 lo, hi;
-            expand16(raw[k], sc[k], lo, hi);
+            expand16(raw[k], logits_part ? sc[k] : sc[k & 2], lo, hi);
             st_shared_v4(tile + piece_at(k) + at0, lo);
             st_shared_v4(tile + piece_at(k) + at1, hi);
           }
