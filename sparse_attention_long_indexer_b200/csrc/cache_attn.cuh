@@ -247,14 +247,14 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   // in the even CTA, arrived on by both
   auto l_full = [&](uint32_t s) { return B(14 + s); };       // its producer warps, a relay: a logits part is in
   auto v_full = [&](uint32_t s) { return B(16 + s); };       // its producer warps, a relay: an output part is in
-  const uint32_t q_full = B(18);                             // producer warps: q is in (TMEM and shared memory)
+  const uint32_t q_full = B(18);                             // a relay: the odd CTA's q is in (TMEM and shared memory)
   auto p_full = [&](uint32_t j) { return B(19 + j); };       // its softmax warps, and the odd CTA's relay
   const uint32_t o_empty = B(21);                            // softmax warps: outputs read
   // in the even CTA only: a logits buffer is free, once the output warp has seen its block's P
   auto s_free = [&](uint32_t i) { return B(22 + i); };       // (3)
   const uint32_t mma_done = B(25);
   // in both CTAs
-  const uint32_t q_read = B(26);                             // producer warps: q is out of the logits ring
+  const uint32_t q_read = B(26);                             // producer warps: q is out of the logits ring, and in
   const uint32_t stored = B(27);                             // softmax warps: an item's outputs are out of the P buffers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -284,7 +284,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
     mbar_init(o_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(q_tma, 1);
-    mbar_init(q_full, 2 * C::PRODUCER_WARPS);
+    mbar_init(q_full, 1);
     mbar_init(q_read, C::PRODUCER_WARPS);
     mbar_init(stored, C::SOFTMAX_WARPS);
     mbar_init(o_empty, 2 * C::SOFTMAX_WARPS);
@@ -440,10 +440,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          arrive_leader(q_full);
-          mbar_arrive(q_read);
-        }
+        if (lane == 0) mbar_arrive(q_read);
         __syncwarp();
         // the ring may be filled once every warp has read its part
         return !logits_part || warp_wait(q_read, q_par, 7);
@@ -708,6 +705,13 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         const bool l_part = warp == static_cast<uint32_t>(C::O_WARP);
         const uint32_t from = logits ? p_local(0) : l_part ? l_local(0) : v_local(0);
         const uint32_t to = lead_off + (logits ? p_full(0) : l_part ? l_full(0) : v_full(0));
+        if (l_part) {                                      // and q
+          if (!warp_wait(q_read, n_busy & 1u, 18)) break;
+          tc_fence_after();
+          tc_fence_before();
+          if (lane == 0) mbar_arrive_cluster(q_full + lead_off);
+          __syncwarp();
+        }
         for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
           const uint32_t st = nb & 1u;
           if (!warp_wait(from + 8u * st, (nb >> 1) & 1u, 11)) { ok = false; break; }
@@ -715,6 +719,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
           __syncwarp();
         }
       } else if (logits) {
+        if (!warp_wait(q_read, n_busy & 1u, 19)) break;
         if (!warp_wait_pair(q_full, n_busy & 1u, 12)) break;
         for (int32_t b = 0; b < n_blocks; ++b, ++nb) {
           const uint32_t st = nb & 1u;
