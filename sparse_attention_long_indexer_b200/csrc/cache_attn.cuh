@@ -20,8 +20,8 @@
 //
 // What bounds it: per 64-row block the two CTAs expand 64K codes, half of them twice (both operands hold a
 // row's latent dims), and every stage of the chain rows -> logits -> softmax -> output hands over through
-// shared memory. 1024 queries of 2048 rows, 128 heads, take 835 us: 699 TFLOP/s, 0.42 of what a bf16 matrix
-// product reaches, at 64% of the issue slots and 32% of the tensor pipe's cycles. Expanding once and
+// shared memory. 1024 queries of 2048 rows, 128 heads, take 791 us: 738 TFLOP/s, 0.45 of what a bf16 matrix
+// product reaches, at 64% of the issue slots and a third of the tensor pipe's cycles. Expanding once and
 // copying the outputs' operand from the logits' with bulk copies within the pair took 0.95 to 1.30 ms: a
 // logits stage then waits for its copy, and the copy for the outputs two blocks back.
 //
@@ -699,13 +699,13 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       if (lane == 0) mbar_arrive(info_empty(slot));
       if (n_blocks == 0) continue;
       if (!leader) {
-        // Relays, one each for P, the logits part and the output part: the odd CTA's warps announce theirs
+        // Relays, one each for P, the logits part and the output part (and q): the odd CTA's warps announce theirs
         // locally, and one cluster-scope arrive, which by cumulativity carries the observed stores, follows.
         // From a producer warp that arrive took 1.5K clocks of every block (a CTA-scope one 0.4K).
         const bool l_part = warp == static_cast<uint32_t>(C::O_WARP);
         const uint32_t from = logits ? p_local(0) : l_part ? l_local(0) : v_local(0);
         const uint32_t to = lead_off + (logits ? p_full(0) : l_part ? l_full(0) : v_full(0));
-        if (l_part) {                                      // and q
+        if (l_part) {
           if (!warp_wait(q_read, n_busy & 1u, 18)) break;
           tc_fence_after();
           tc_fence_before();

@@ -833,15 +833,15 @@ int row_grid(int64_t rows, int sms) {
 
 // How the rows of a query are split (see cache_attn.cuh): by the least cost of the slowest pair of SMs,
 // whose items follow one another, and of the join. Measured at the production dims: an item takes 9 us
-// beside its blocks (list, q, first loads, output) and 1.6 us per block; a join 2 us, 0.1 us per range
-// of a query and 0.05 us per range of all queries (256 KB written and read). One query of 2048 rows in
-// 1 / 8 / 16 / 32 ranges: 63.2 / 21.5 / 19.7 / 21.3 us; 16 queries in 1 / 4 / 8: 64.1 / 32.1 / 39.6 us;
-// 64 queries in 1 / 2: 70 / 87 us. The pairs are this rule's, not the device's: it also sizes workspaces.
+// beside its blocks (list, q, first loads, output) and 1.45 us per block; a join 2 us, 0.1 us per range
+// of a query and 0.08 us per range of all queries (256 KB written and read). One query of 2048 rows in
+// 1 / 8 / 16 / 32 ranges: 57.5 / 20.6 / 18.8 / 21.2 us; 16 queries in 1 / 4 / 8: 58.5 / 31.0 / 39.7 us;
+// 64 queries in 1 / 2: 63 / 82 us. The pairs are this rule's, not the device's: it also sizes workspaces.
 struct CachePlan {
   int32_t n_splits, split_blocks;
 };
 constexpr int64_t kPlanPairs = 74;
-constexpr int64_t kPlanItemNs = 9000, kPlanBlockNs = 1600, kPlanJoinNs = 2000, kPlanRangeNs = 100, kPlanPartNs = 50;
+constexpr int64_t kPlanItemNs = 9000, kPlanBlockNs = 1450, kPlanJoinNs = 2000, kPlanRangeNs = 100, kPlanPartNs = 80;
 CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
   CachePlan best{1, 1};
   const int64_t queries = static_cast<int64_t>(d.batch) * d.n_q;
