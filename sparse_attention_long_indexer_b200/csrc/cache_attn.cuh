@@ -20,8 +20,8 @@
 //
 // What bounds it: per 64-row block the two CTAs expand 64K codes, half of them twice (both operands hold a
 // row's latent dims), and every stage of the chain rows -> logits -> softmax -> output hands over through
-// shared memory. 1024 queries of 2048 rows, 128 heads, take 791 us: 738 TFLOP/s, 0.45 of what a bf16 matrix
-// product reaches, at 64% of the issue slots and a third of the tensor pipe's cycles. Expanding once and
+// shared memory. 1024 queries of 2048 rows, 128 heads, take 788 us: 741 TFLOP/s, 0.45 of what a bf16 matrix
+// product reaches, at 63% of the issue slots and 34% of the tensor pipe's cycles. Expanding once and
 // copying the outputs' operand from the logits' with bulk copies within the pair took 0.95 to 1.30 ms: a
 // logits stage then waits for its copy, and the copy for the outputs two blocks back.
 //
