@@ -25,7 +25,7 @@ constexpr int kScaleGroup = 128;         // latent dims per scale
 constexpr int kScaleExpMax = 100;        // |exponent| of a scale
 constexpr int kRowThreads = 256;         // 8 warps = 8 rows per CTA and pass
 constexpr int kRowWarps = kRowThreads / 32;
-// Resident CTAs per SM, and the most that are launched. 32768 rows written take 16.3 us (4.4 TB/s of the
+// Resident CTAs per SM, and the most that are launched. 32768 rows written take 16.1 us (4.5 TB/s of the
 // 6.5 a copy reaches); with 8 launched per SM, of which 6 fit, 18.3, and with the next row's loads ahead of
 // the current row's stores, at 4 per SM, 18.2.
 constexpr int kRowCtas = 6;
@@ -89,9 +89,9 @@ __device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, uint64_t inv2
   return r;
 }
 // Two E4M3 codes times a scale (packed twice), as two bf16. Codes convert to fp16 and fp16 to fp32
-// exactly; the product with a power of two, and its bf16 form, are exact too. 16 codes a word of four
-// at 3.0 clk per SM and warp instruction; moving sign, exponent and mantissa into a bf16's places and
-// multiplying there takes fewer instructions but 4.5 clk, as most of them are integer ones.
+// exactly; the product with a power of two, and its bf16 form, are exact too. An SM takes 3.0 clocks for a
+// warp's words of four codes; moving sign, exponent and mantissa into a bf16's places and multiplying
+// there takes fewer instructions but 4.5 clocks, as most of them are integer ones.
 __device__ __forceinline__ uint32_t expand2(uint16_t codes, uint64_t scale2) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
