@@ -252,8 +252,8 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   const uint32_t o_empty = B(21);                            // softmax warps: outputs read
   // in the even CTA only: a logits buffer is free, once the output warp has seen its block's P
   auto s_free = [&](uint32_t i) { return B(22 + i); };       // (3)
-  const uint32_t mma_done = B(25);
   // in both CTAs
+  const uint32_t mma_done = B(25);                           // the MMA warps' last commits
   const uint32_t q_read = B(26);                             // producer warps: q is out of the logits ring, and in
   const uint32_t stored = B(27);                             // softmax warps: an item's outputs are out of the P buffers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -678,8 +678,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         nb += static_cast<uint32_t>(n_list + n_tail);
       }
     }
-    // after an abort the q copy in flight lands before the CTA may leave (else it has landed)
-    if (lane == 0 && n_busy > 0 && wt.aborted()) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
+    // The last q copy lands before the CTA may leave. Whoever waits for it may give up, and raise the abort
+    // flag, only after this warp has come here, so the flag says nothing about it.
+    if (lane == 0 && n_busy > 0) attn_drain_wait(q_tma, (n_busy - 1) & 1u, kDrainBudgetNs);
   } else if (warp >= static_cast<uint32_t>(C::S_WARP)) {
     // ================================================================ MMA issuers (even CTA), relays (odd CTA)
     // One warp issues the logits MMAs, one the output MMAs, so that each one's waits (issue blocks
@@ -781,7 +782,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
       ++n_busy;
     }
     if (leader && warp != static_cast<uint32_t>(C::R_WARP) && elect_one()) {
-      commit2(mma_done);
+      commit_pair(mma_done);
       attn_drain_wait(mma_done, 0, kDrainBudgetNs);
     }
   } else {
@@ -1049,6 +1050,9 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
   __syncthreads();
   cluster_sync();            // no CTA leaves while its peer may still use its memory
   if (warp == C::S_WARP) {
+    // The odd CTA has no MMAs of its own, but the even one's commits arrive on its barriers, and after an
+    // abort nobody may have waited for them. By now the last ones have been issued and are over in the even CTA.
+    if (!leader) attn_drain_wait(mma_done, 0, kDrainBudgetNs);
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
