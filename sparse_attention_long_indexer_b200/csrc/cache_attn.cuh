@@ -1062,33 +1062,53 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
 // Joins the ranges of a query: with l_s the log-sum-exp of range s (log2 domain) and o_s its
 // normalised output, w_s = 2^(l_s - max l), out = sum w_s o_s / sum w_s, lse = max l + log2 sum w_s.
 // One CTA per (query, head), four dims per thread; a range without a row (l_s = -inf) wrote no
-// output and is not read.
+// output, and what is read in its place is not used.
+//
+// This kernel starts while the ranges' kernel still writes what it reads. So its loads are plain ones, behind the
+// wait: the read-only path (__ldg, or const pointers that nothing else may alias) is for data that does not change
+// while a kernel runs, and the compiler may move such loads up past the wait. They are issued kJoinBatch ranges
+// at a time, without a condition between them: one query of 2048 rows takes 18.1 us (18.9 with __ldg, 21.2 with plain
+// loads each under its range's condition).
 constexpr int kJoinThreads = 128;
+constexpr int kJoinBatch = 8;
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(
-    const float* __restrict__ part_out, const float* __restrict__ part_lse, __nv_bfloat16* __restrict__ out,
-    float* __restrict__ lse, int32_t n_splits, int32_t n_heads, int32_t d_latent) {
+    const float* part_out, const float* part_lse, __nv_bfloat16* out, float* lse, int32_t n_splits, int32_t n_heads,
+    int32_t d_latent) {
   asm volatile("griddepcontrol.wait;" ::: "memory");    // the ranges' kernel is done and its stores are visible
   const int64_t row = blockIdx.x;                        // (query, head)
   const int64_t qi = row / n_heads, head = row - qi * n_heads;
   const float* lrow = part_lse + qi * n_splits * n_heads + head;
-  float mx = -INFINITY;
-  for (int32_t s = 0; s < n_splits; ++s) mx = fmaxf(mx, __ldg(lrow + static_cast<int64_t>(s) * n_heads));
-  float total = 0.f;
-  const float msub = mx == -INFINITY ? 0.f : mx;
   const int32_t dim = 4 * static_cast<int32_t>(threadIdx.x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* orow = part_out + (qi * n_splits * n_heads + head) * d_latent + (dim < d_latent ? dim : 0);
+  const int64_t step = static_cast<int64_t>(n_heads) * d_latent;
+  float l[kJoinBatch];
+  float4 o[kJoinBatch];
+  auto fetch = [&](int32_t s0) {
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      const int32_t s = min(s0 + u, n_splits - 1);
+      l[u] = lrow[static_cast<int64_t>(s) * n_heads];
+      o[u] = *reinterpret_cast<const float4*>(orow + s * step);
+    }
+  };
+  fetch(0);
+  float mx = -INFINITY;
 #pragma unroll 8
-  for (int32_t s = 0; s < n_splits; ++s) {
-    const float l = __ldg(lrow + static_cast<int64_t>(s) * n_heads);
-    const float w = exp2f(l - msub);
-    total += w;
-    if (l != -INFINITY && dim < d_latent) {
-      const float4 o = __ldg(reinterpret_cast<const float4*>(
-          part_out + ((qi * n_splits + s) * n_heads + head) * d_latent + dim));
-      acc.x += w * o.x;
-      acc.y += w * o.y;
-      acc.z += w * o.z;
-      acc.w += w * o.w;
+  for (int32_t s = 0; s < n_splits; ++s) mx = fmaxf(mx, lrow[static_cast<int64_t>(s) * n_heads]);
+  const float msub = mx == -INFINITY ? 0.f : mx;
+  float total = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int32_t s0 = 0; s0 < n_splits; s0 += kJoinBatch) {
+    if (s0 > 0) fetch(s0);
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      if (s0 + u >= n_splits || l[u] == -INFINITY) continue;
+      const float w = exp2f(l[u] - msub);
+      total += w;
+      acc.x += w * o[u].x;
+      acc.y += w * o[u].y;
+      acc.z += w * o[u].z;
+      acc.w += w * o[u].w;
     }
   }
   const float inv = total == 0.f ? 0.f : 1.0f / total;
