@@ -38,7 +38,7 @@
 //    what its own warps have ready.
 //  * softmax: 4 warps; lane L has rows 32 (L / 64) .. +31 of a block of head L % 64 of this CTA.
 //    Online softmax in the log2 domain; the running max is raised, and the output rescaled, only when
-//    it grows by more than kLazyRescale.
+//    it grows by more than kRescaleSlack.
 // Statistics and outputs are fp32; P is rounded to bf16 for the tensor core. The output is
 // normalised by the sum of the rounded weights (so they add up to one), lse takes the unrounded.
 #pragma once
@@ -52,6 +52,10 @@
 namespace dsa {
 
 constexpr int kMaxDraft = 256;           // nodes of a drafted tree
+// How far (log2) the running max may lag behind a block's before it is raised and the outputs so far are rescaled: a
+// weight is at most 2^kRescaleSlack, so that 2048 listed and 256 drafted rows of the cache's largest magnitude,
+// 448 * 2^100, sum up to 2304 * 2^7 * 448 * 2^100 < 2^127, half of what fp32 holds.
+constexpr float kRescaleSlack = 7.0f;
 
 struct CacheAttnCfg {
   static constexpr int BLK = 64;                         // rows per block
@@ -878,7 +882,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap map_q, const CacheAttnPara
         float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;     // sc > 0
         mb = fmaxf(mb, swap_partner(mb));
         if (!ok) break;
-        const bool need = mb > m2 + kLazyRescale;
+        const bool need = mb > m2 + kRescaleSlack;
         float alpha = 1.0f;
         if (need) {
           alpha = m2 == -INFINITY ? 0.0f : ex2_approx(m2 - mb);
