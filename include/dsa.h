@@ -214,7 +214,9 @@ typedef struct {
 
 /* Bytes of workspace that dsa_sparse_mla_attn_qcache, dsa_tree_mla_attn and
  * dsa_tree_mla_attn_qcache need for these dims and top-k (256-byte aligned pointer required;
- * initialise it with dsa_workspace_init). dsa_qcache_write and dsa_qcache_read use the status word
+ * initialise it with dsa_workspace_init). It holds the ranges that a call with few queries is split into, and never
+ * shrinks as batch, n_q, topk, n_heads or d_latent grow: one made for the largest sizes serves every smaller call
+ * (49 MB at most at the production dims). dsa_qcache_write and dsa_qcache_read use the status word
  * only: 256 bytes of any workspace. Returns 0 for invalid dims. Pure host function. */
 size_t dsa_qcache_workspace_bytes(const dsa_dims* dims, int32_t topk);
 

@@ -251,7 +251,7 @@ class Workspace:
 
     @staticmethod
     def create_qcache(dims: dsa_dims, topk: int, device=None, stream=None) -> "Workspace":
-        """A workspace for the calls on an 8-bit cache and on drafted trees."""
+        """A workspace for the calls on an 8-bit cache and on drafted trees, of these sizes and smaller ones."""
         n = dsa_qcache_workspace_bytes(dims, topk)
         if n == 0:
             raise DSAError(DSA_ERR_INVALID_ARG, "dsa_qcache_workspace_bytes")

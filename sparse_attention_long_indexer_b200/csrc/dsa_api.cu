@@ -836,11 +836,14 @@ int row_grid(int64_t rows, int sms) {
 // beside its blocks (list, q, first loads, output) and 1.45 us per block; a join 2 us, 0.1 us per range
 // of a query and 0.08 us per range of all queries (256 KB written and read). One query of 2048 rows in
 // 1 / 8 / 16 / 32 ranges: 57.5 / 20.6 / 18.8 / 21.2 us; 16 queries in 1 / 4 / 8: 58.5 / 31.0 / 39.7 us;
-// 64 queries in 1 / 2: 63 / 82 us. The pairs are this rule's, not the device's: it also sizes workspaces.
+// 64 queries in 1 / 2: 63 / 82 us. The pairs are this rule's, not the device's. By these costs no call is split into
+// more than kPlanParts ranges of all its queries (93 queries in two each; more queries are not split), so the
+// limit changes no choice: it is what a workspace has to hold (see cache_workspace).
 struct CachePlan {
   int32_t n_splits, split_blocks;
 };
 constexpr int64_t kPlanPairs = 74;
+constexpr int64_t kPlanParts = 186;
 constexpr int64_t kPlanItemNs = 9000, kPlanBlockNs = 1450, kPlanJoinNs = 2000, kPlanRangeNs = 100, kPlanPartNs = 80;
 CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
   CachePlan best{1, 1};
@@ -851,7 +854,7 @@ CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
   int64_t least = -1;
   for (int32_t per = blocks; per >= 1; --per) {
     const int32_t splits = (blocks + per - 1) / per;
-    if (least >= 0 && splits == best.n_splits) continue;
+    if (least >= 0 && (splits == best.n_splits || queries * splits > kPlanParts)) continue;
     const int64_t waves = (queries * splits + kPlanPairs - 1) / kPlanPairs;
     int64_t cost = waves * (kPlanItemNs + per * kPlanBlockNs);
     if (splits > 1) cost += kPlanJoinNs + kPlanRangeNs * splits + kPlanPartNs * queries * splits;
@@ -864,20 +867,26 @@ CachePlan plan_cache(const dsa_dims& d, int32_t topk, bool tree) {
   return best;
 }
 
-// Workspace of the attention calls on caches: status word, then the ranges' outputs and statistics.
+// Workspace of the attention calls on caches: status word, then the outputs and statistics of `parts` ranges.
 struct CacheLayout {
   size_t part_out = 0, part_lse = 0, total = 0;
 };
-CacheLayout cache_layout(const dsa_dims& d, const CachePlan& plan) {
+CacheLayout cache_layout(const dsa_dims& d, int64_t parts) {
   CacheLayout L;
   size_t off = kAlign;
-  if (plan.n_splits > 1) {
-    const size_t rows = static_cast<size_t>(d.batch) * d.n_q * plan.n_splits * d.n_heads;
-    L.part_out = off; off = align_up(off + rows * d.d_latent * 4);
-    L.part_lse = off; off = align_up(off + rows * 4);
-  }
+  const size_t rows = static_cast<size_t>(parts) * d.n_heads;
+  L.part_out = off; off = align_up(off + rows * d.d_latent * 4);
+  L.part_lse = off; off = align_up(off + rows * 4);
   L.total = off;
   return L;
+}
+// What these dims and every smaller ones need, in each form of the calls: few queries are split and many are not, so the
+// need of one call does not grow with its sizes, but a workspace is made once and a batch shrinks. A query has at
+// most as many ranges as blocks.
+size_t cache_workspace(const dsa_dims& d, int32_t topk) {
+  const int64_t blocks = (topk + CacheAttnCfg::BLK - 1) / CacheAttnCfg::BLK +
+                         (std::min(d.n_q, kMaxDraft) + CacheAttnCfg::BLK - 1) / CacheAttnCfg::BLK;
+  return cache_layout(d, std::min(static_cast<int64_t>(d.batch) * d.n_q * blocks, kPlanParts)).total;
 }
 
 template <bool kQuant, bool kTree>
@@ -898,8 +907,8 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   if (tree && d.n_q > kMaxDraft) return DSA_ERR_UNSUPPORTED;
   const int64_t queries = static_cast<int64_t>(d.batch) * d.n_q;
   const CachePlan plan = plan_cache(d, topk, tree);
-  const CacheLayout L = cache_layout(d, plan);
-  if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
+  const CacheLayout L = cache_layout(d, plan.n_splits > 1 ? queries * plan.n_splits : 0);
+  if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < cache_workspace(d, topk)) return DSA_ERR_WORKSPACE;
   if (queries == 0) return DSA_OK;
   if (queries * d.n_heads >= (int64_t(1) << 31) || queries * plan.n_splits >= (int64_t(1) << 31))
     return DSA_ERR_UNSUPPORTED;
@@ -964,10 +973,7 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
 extern "C" {
 
 size_t dsa_qcache_workspace_bytes(const dsa_dims* dims, int32_t topk) {
-  if (check_dims(dims, topk) != DSA_OK) return 0;
-  const size_t listed = cache_layout(*dims, plan_cache(*dims, topk, false)).total;
-  if (dims->n_q > kMaxDraft) return listed;
-  return std::max(listed, cache_layout(*dims, plan_cache(*dims, topk, true)).total);
+  return check_dims(dims, topk) == DSA_OK ? cache_workspace(*dims, topk) : 0;
 }
 
 dsa_status dsa_qcache_write(const dsa_dims* dims, const void* latent, const void* keys, int32_t n_src,
