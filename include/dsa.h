@@ -205,6 +205,9 @@ dsa_status dsa_indexer_topk_decode_noalloc(const dsa_dims* dims, const void* q_i
  * gets the scale NaN and reads as NaN throughout. code * scale is exact in bf16. In a cache filled by
  * other means a scale may be any fp32: a value is then code * scale rounded to fp32 and to bf16.
  * The calls on an 8-bit cache require d_latent % 16 == 0 (else DSA_ERR_UNSUPPORTED).
+ * dsa_qcache_write and dsa_qcache_read move n_q rows per sequence, which may be more than max_len, and use
+ * idx_dim (written keys only), d_latent and d_rope of the other dims. In the attention calls n_q <= max_len
+ * holds as everywhere, for the nodes of a drafted tree too.
  */
 typedef struct {
   void* codes;    /* E4M3 [B, max_len, d_latent]                  (16-byte aligned) */

@@ -109,7 +109,8 @@ bool is_production(const dsa_dims& d) {
          d.d_rope == kDqk - kDv;
 }
 
-dsa_status check_dims(const dsa_dims* d, int32_t topk) {
+// dims of a call, but for what the decode selection alone is limited to
+dsa_status check_shape(const dsa_dims* d, int32_t topk) {
   if (d == nullptr) return DSA_ERR_INVALID_ARG;
   if (d->batch < 0 || d->n_q < 0 || d->max_len < 0) return DSA_ERR_INVALID_ARG;
   if (d->n_q > d->max_len) return DSA_ERR_INVALID_ARG;
@@ -122,6 +123,12 @@ dsa_status check_dims(const dsa_dims* d, int32_t topk) {
   if (d->n_heads > kHeads || d->d_latent > kDv || d->d_latent % 8 != 0) return DSA_ERR_UNSUPPORTED;
   if (d->d_rope > kDqk - kDv || d->d_rope % 8 != 0) return DSA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->batch) * d->max_len > (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+dsa_status check_dims(const dsa_dims* d, int32_t topk) {
+  const dsa_status s = check_shape(d, topk);
+  if (s != DSA_OK) return s;
   if (d->n_q == 1 && (d->max_len + kDecodeChunk - 1) / kDecodeChunk > 1024) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
@@ -803,11 +810,25 @@ extern "C" dsa_status dsa_indexer_topk_decode_noalloc(const dsa_dims* dims, cons
 // ----------------------------------------------------------------------------- 8-bit cache, drafted trees
 namespace {
 
-// dims of the calls on an 8-bit cache: whole 16-byte chunks of codes
-dsa_status check_dims8(const dsa_dims* dims, int32_t topk) {
-  const dsa_status s = check_dims(dims, topk);
+// dims of the attention over an 8-bit cache: whole 16-byte chunks of codes
+dsa_status check_shape8(const dsa_dims* dims, int32_t topk) {
+  const dsa_status s = check_shape(dims, topk);
   if (s != DSA_OK) return s;
   return dims->d_latent % 16 == 0 ? DSA_OK : DSA_ERR_UNSUPPORTED;
+}
+
+// dims of the calls that move rows: n_q is their number and has nothing to do with max_len, and no indexer or
+// attention runs (keys: idx_dim is used)
+dsa_status check_row_dims(const dsa_dims* d, bool keys) {
+  if (d == nullptr) return DSA_ERR_INVALID_ARG;
+  if (d->batch < 0 || d->n_q < 0 || d->max_len < 0) return DSA_ERR_INVALID_ARG;
+  if (d->d_latent < 1 || d->d_rope < 0 || (keys && d->idx_dim < 1)) return DSA_ERR_INVALID_ARG;
+  if (d->d_latent > kDv || d->d_latent % 16 != 0) return DSA_ERR_UNSUPPORTED;
+  if (d->d_rope > kDqk - kDv || d->d_rope % 8 != 0) return DSA_ERR_UNSUPPORTED;
+  if (keys && (d->idx_dim > kIdxDim || d->idx_dim % 16 != 0)) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d->batch) * d->max_len > (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d->batch) * d->n_q > (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
 }
 
 dsa_status check_qcache(const dsa_dims& d, const dsa_qcache* c) {
@@ -900,7 +921,7 @@ dsa_status launch_cache_attn(const CUtensorMap& map_q, const CacheAttnParams& p,
 dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache* cache, const void* kv,
                            const int32_t* idx, int32_t topk, bool tree, const void* draft, const int32_t* parents,
                            void* out, float* lse, void* ws, size_t ws_bytes, dsa_stream_t stream) {
-  dsa_status s = cache != nullptr ? check_dims8(dims, topk) : check_dims(dims, topk);
+  dsa_status s = cache != nullptr ? check_shape8(dims, topk) : check_shape(dims, topk);
   if (s != DSA_OK) return s;
   const dsa_dims& d = *dims;
   if (!(d.softmax_scale > 0.f)) return DSA_ERR_INVALID_ARG;
@@ -973,7 +994,7 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
 extern "C" {
 
 size_t dsa_qcache_workspace_bytes(const dsa_dims* dims, int32_t topk) {
-  return check_dims(dims, topk) == DSA_OK ? cache_workspace(*dims, topk) : 0;
+  return check_shape(dims, topk) == DSA_OK ? cache_workspace(*dims, topk) : 0;
 }
 
 dsa_status dsa_qcache_write(const dsa_dims* dims, const void* latent, const void* keys, int32_t n_src,
@@ -981,7 +1002,7 @@ dsa_status dsa_qcache_write(const dsa_dims* dims, const void* latent, const void
                             const dsa_qcache* cache, void* k_idx, float* k_scale, void* ws, size_t ws_bytes,
                             dsa_stream_t stream) {
   NvtxRange range("qcache_write");
-  dsa_status s = check_dims8(dims, 1);
+  dsa_status s = check_row_dims(dims, keys != nullptr);
   if (s != DSA_OK) return s;
   const dsa_dims& d = *dims;
   if (n_src < 0 || (src_rows == nullptr && n_src < d.n_q)) return DSA_ERR_INVALID_ARG;
@@ -1020,7 +1041,7 @@ dsa_status dsa_qcache_read(const dsa_dims* dims, const dsa_qcache* cache, const 
                            const int32_t* start, const int32_t* lengths, void* out, void* ws, size_t ws_bytes,
                            dsa_stream_t stream) {
   NvtxRange range("qcache_read");
-  dsa_status s = check_dims8(dims, 1);
+  dsa_status s = check_row_dims(dims, false);
   if (s != DSA_OK) return s;
   const dsa_dims& d = *dims;
   if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
