@@ -304,7 +304,7 @@ dsa_status dsa_get_device_status(void* ws, dsa_stream_t stream, uint32_t* detail
 /*
  * Test setting for failure detection: the time budget of every bounded wait in the pipelines of the
  * indexer (dsa_indexer_topk*, forward's first stage) and of the attention over an 8-bit cache or a
- * drafted tree, in ns; 0 restores the default of 2 s.
+ * drafted tree (there a minute at most), in ns; 0 restores the default of 2 s.
  * Process-wide, read at each launch. With a budget too short for the pipeline's handshakes a
  * launch stops early: its waits record DSA_ERR_DEVICE_TIMEOUT in the status word, every role
  * ends, the teardown still lets in-flight copies and MMAs land (under their own fixed budget),

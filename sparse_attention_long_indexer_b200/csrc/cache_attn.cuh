@@ -56,6 +56,9 @@ constexpr int kMaxDraft = 256;           // nodes of a drafted tree
 // weight is at most 2^kRescaleSlack, so that 2048 listed and 256 drafted rows of the cache's largest magnitude,
 // 448 * 2^100, sum up to 2304 * 2^7 * 448 * 2^100 < 2^127, half of what fp32 holds.
 constexpr float kRescaleSlack = 7.0f;
+// The longest budget of a wait, a minute: every wait has an end, and 2 clocks per ns stay far within the 63 bits that the
+// waits count in.
+constexpr uint64_t kMaxCacheWaitNs = 60000000000ull;
 
 struct CacheAttnCfg {
   static constexpr int BLK = 64;                         // rows per block

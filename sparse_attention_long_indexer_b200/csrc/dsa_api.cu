@@ -965,7 +965,7 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   p.split_blocks = plan.split_blocks;
   p.n_items = static_cast<int32_t>(queries * plan.n_splits);
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
-  p.wait_budget_ns = g_indexer_wait_ns.load(std::memory_order_relaxed);
+  p.wait_budget_ns = std::min(g_indexer_wait_ns.load(std::memory_order_relaxed), kMaxCacheWaitNs);
   CUtensorMap map_q;
   if (!encode_q_rows(&map_q, q, static_cast<uint64_t>(queries) * d.n_heads,
                      static_cast<uint64_t>(d.d_latent + d.d_rope)))

@@ -70,3 +70,18 @@ def test_launches_that_end_early_leave_nothing_in_flight(kind, n, topk):
         out, lse = call()
         ws.check()
     right(out, lse)
+
+
+# the widest numbers of a budget, held to a minute: as signed clocks, two to the ns, those from 2^62 on would have
+# passed already
+@pytest.mark.parametrize("ns", [10 ** 9, 2 ** 62 - 1, 2 ** 62, 2 ** 63, 2 ** 64 - 1])
+def test_a_long_budget_is_a_long_one(ns):
+    call, right, ws = _case("listed", 74, 128, 61)
+    dsa.dsa_set_wait_budget_ns(ns)
+    try:
+        out, lse = call()
+        torch.cuda.synchronize()
+    finally:
+        dsa.dsa_set_wait_budget_ns(0)
+    ws.check()
+    right(out, lse)
