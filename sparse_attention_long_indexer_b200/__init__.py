@@ -357,6 +357,16 @@ def _call_device(t: torch.Tensor) -> int:
     return device
 
 
+def _workspace(ws: Workspace, device: int) -> torch.Tensor:
+    """A workspace's buffer, checked like the call's tensors: kernels write to it."""
+    buf = ws.buf
+    if buf.dtype is not torch.uint8:
+        raise TypeError(f"workspace: expected torch.uint8, got {buf.dtype}")
+    if buf.get_device() != device:
+        raise ValueError(f"the workspace is on {buf.device}, the call runs on cuda:{device}")
+    return buf
+
+
 @dataclass
 class QCache:
     """An 8-bit latent cache (see ``dsa_qcache`` in ``include/dsa.h``), with the index keys beside it.
@@ -432,8 +442,8 @@ def qcache_write(dims, cache: QCache, latent, keys, ws: Workspace, start=None, l
         _same("src_rows", src_rows, torch.int32, dims.batch * dims.n_q, device)
     _per_sequence(dims, device, start=start, lengths=lengths)
     dsa_qcache_write(dims, latent, keys, n_src, src_rows, start, lengths, cache._struct(dims, device),
-                     cache.k_idx if keys is not None else None, cache.k_scale if keys is not None else None, ws.buf,
-                     stream)
+                     cache.k_idx if keys is not None else None, cache.k_scale if keys is not None else None,
+                     _workspace(ws, device), stream)
 
 
 def qcache_read(dims, cache: QCache, ws: Workspace, rows=None, start=None, lengths=None, stream=None):
@@ -445,7 +455,7 @@ def qcache_read(dims, cache: QCache, ws: Workspace, rows=None, start=None, lengt
     _per_sequence(dims, device, start=start, lengths=lengths)
     with _allocating(stream):
         out = cache.rope.new_empty((dims.batch, dims.n_q, dims.d_latent + dims.d_rope))
-    dsa_qcache_read(dims, cache._struct(dims, device), rows, start, lengths, out, ws.buf, stream)
+    dsa_qcache_read(dims, cache._struct(dims, device), rows, start, lengths, out, _workspace(ws, device), stream)
     return out
 
 
@@ -463,7 +473,8 @@ def _attention_inputs(dims, q, idx, topk, stream):
 def sparse_mla_attn_qcache(dims, q, cache: QCache, idx, topk, ws: Workspace, stream=None):
     """``sparse_mla_attn`` over an 8-bit cache. Returns (out bf16 [B, n_q, H, d_latent], lse fp32 [B, n_q, H])."""
     device, out, lse = _attention_inputs(dims, q, idx, topk, stream)
-    dsa_sparse_mla_attn_qcache(dims, q, cache._struct(dims, device), idx, topk, out, lse, ws.buf, stream)
+    dsa_sparse_mla_attn_qcache(dims, q, cache._struct(dims, device), idx, topk, out, lse, _workspace(ws, device),
+                               stream)
     return out, lse
 
 
@@ -477,11 +488,11 @@ def tree_mla_attn(dims, q, cache, idx, topk, draft, parents, ws: Workspace, stre
     _same("draft", draft, torch.bfloat16, dims.batch * dims.n_q * width, device)
     _same("parents", parents, torch.int32, dims.batch * dims.n_q, device)
     if isinstance(cache, QCache):
-        dsa_tree_mla_attn_qcache(dims, q, cache._struct(dims, device), idx, topk, draft, parents, out, lse, ws.buf,
-                                 stream)
+        dsa_tree_mla_attn_qcache(dims, q, cache._struct(dims, device), idx, topk, draft, parents, out, lse,
+                                 _workspace(ws, device), stream)
     else:
         _same("cache", cache, torch.bfloat16, dims.batch * dims.max_len * width, device)
-        dsa_tree_mla_attn(dims, q, cache, idx, topk, draft, parents, out, lse, ws.buf, stream)
+        dsa_tree_mla_attn(dims, q, cache, idx, topk, draft, parents, out, lse, _workspace(ws, device), stream)
     return out, lse
 
 
