@@ -18,7 +18,7 @@
 // which needs no cluster but computes and expands everything for the logits twice, took 1.67 ms for
 // 1024 queries of 2048 rows.)
 //
-// What bounds it: per 64-row block the two CTAs expand 64K codes, half of them twice (both operands hold a
+// What bounds it: per 64-row block the two CTAs expand 32K codes, each of them twice (both operands hold a
 // row's latent dims), and every stage of the chain rows -> logits -> softmax -> output hands over through
 // shared memory. 1024 queries of 2048 rows, 128 heads, take 788 us: 741 TFLOP/s, 0.45 of what a bf16 matrix
 // product reaches, at 63% of the issue slots and 34% of the tensor pipe's cycles. Expanding once and
@@ -99,10 +99,10 @@ struct CacheAttnCfg {
 };
 
 struct CacheAttnParams {
-  const __nv_bfloat16* q;        // [T, n_heads, d_latent + d_rope], T = B * n_q
+  uint64_t wait_budget_ns;
   const __nv_bfloat16* kv;       // bf16 cache [B, max_len, d_latent + d_rope]
   QCacheView cache;              // 8-bit cache
-  const int32_t* idx;            // [T, topk]
+  const int32_t* idx;            // [T, topk], T = B * n_q
   const __nv_bfloat16* draft;    // [B, n_q, d_latent + d_rope]
   const int32_t* parents;        // [B, n_q]
   __nv_bfloat16* out;            // [T, n_heads, d_latent]
@@ -113,7 +113,6 @@ struct CacheAttnParams {
   int32_t n_q, max_len, topk, n_heads, d_latent, d_rope;
   int32_t n_splits, split_blocks, n_items;
   float scale_log2;              // tau * log2(e), positive
-  uint64_t wait_budget_ns;
 };
 
 // Arrives once on the barrier at this offset in both CTAs of the pair when every 2-SM MMA this thread

@@ -944,7 +944,6 @@ dsa_status cache_attention(const dsa_dims* dims, const void* q, const dsa_qcache
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   CacheAttnParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
   p.kv = static_cast<const __nv_bfloat16*>(kv);
   if (cache != nullptr) p.cache = view(*cache);
   p.idx = idx;
