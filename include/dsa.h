@@ -266,8 +266,9 @@ dsa_status dsa_qcache_read(const dsa_dims* dims, const dsa_qcache* cache, const 
  * duplicates included), with the rows' values as dsa_qcache_read gives them. A query's rows are
  * split over several CTAs when there are few queries (decode). softmax_scale must be positive.
  * The sums are fp32: rows of magnitudes up to 448 * 2^100, the largest that dsa_qcache_write leaves, do not
- * overflow them as long as q . kv itself is within fp32. The same holds for the calls on trees, whose drafted
- * rows and bf16 caches may hold larger ones: outputs are then infinities or NaN where a sum overflows.
+ * overflow them as long as q . kv and tau * log2(e) times it are within fp32. The same holds for the calls
+ * on trees, whose drafted rows and bf16 caches may hold larger ones: outputs are then infinities or NaN where
+ * a sum overflows.
  * Workspace: dsa_qcache_workspace_bytes.
  */
 dsa_status dsa_sparse_mla_attn_qcache(const dsa_dims* dims, const void* q, const dsa_qcache* cache,

@@ -20,10 +20,11 @@
 //
 // What bounds it: per 64-row block the two CTAs expand 32K codes, each of them twice (both operands hold a
 // row's latent dims), and every stage of the chain rows -> logits -> softmax -> output hands over through
-// shared memory. 1024 queries of 2048 rows, 128 heads, take 788 us: 741 TFLOP/s, 0.45 of what a bf16 matrix
-// product reaches, at 63% of the issue slots and 34% of the tensor pipe's cycles. Expanding once and
-// copying the outputs' operand from the logits' with bulk copies within the pair took 0.95 to 1.30 ms: a
-// logits stage then waits for its copy, and the copy for the outputs two blocks back.
+// shared memory. 1024 queries of 2048 rows, 128 heads, take 776 us (850 in a long row of calls, under the power
+// cap): 753 TFLOP/s, 0.46 of what a bf16 matrix product reaches, at 64% of the issue slots and 35% of the tensor
+// pipe's cycles. Of that, 126 us are the 14 items of a pair beside their blocks. Expanding once and copying the
+// outputs' operand from the logits' with bulk copies within the pair took 0.95 to 1.30 ms: a logits stage then
+// waits for its copy, and the copy for the outputs two blocks back.
 //
 // One CTA, 24 warps:
 //  * control (1 warp): how far the range's list reaches, a node's path, and the item's q, ahead of the item.
@@ -56,8 +57,8 @@ constexpr int kMaxDraft = 256;           // nodes of a drafted tree
 // weight is at most 2^kRescaleSlack, so that 2048 listed and 256 drafted rows of the cache's largest magnitude,
 // 448 * 2^100, sum up to 2304 * 2^7 * 448 * 2^100 < 2^127, half of what fp32 holds.
 constexpr float kRescaleSlack = 7.0f;
-// The longest budget of a wait, a minute: every wait has an end, and 2 clocks per ns stay far within the 63 bits that the
-// waits count in.
+// The longest budget of a wait, a minute: every wait has an end, and 2 clocks per ns stay far within the 63 bits
+// that the waits count in.
 constexpr uint64_t kMaxCacheWaitNs = 60000000000ull;
 
 struct CacheAttnCfg {

@@ -856,10 +856,12 @@ int row_grid(int64_t rows, int sms) {
 // whose items follow one another, and of the join. Measured at the production dims: an item takes 9 us
 // beside its blocks (list, q, first loads, output) and 1.45 us per block; a join 2 us, 0.1 us per range
 // of a query and 0.08 us per range of all queries (256 KB written and read). One query of 2048 rows in
-// 1 / 8 / 16 / 32 ranges: 57.5 / 20.6 / 18.8 / 21.2 us; 16 queries in 1 / 4 / 8: 58.5 / 31.0 / 39.7 us;
-// 64 queries in 1 / 2: 63 / 82 us. The pairs are this rule's, not the device's. By these costs no call is split into
-// more than kPlanParts ranges of all its queries (93 queries in two each; more queries are not split), so the
-// limit changes no choice: it is what a workspace has to hold (see cache_workspace).
+// 1 / 8 / 16 / 32 ranges: 57.9 / 19.7 / 17.8 / 20.5 us; 16 queries in 1 / 4 / 8: 58.5 / 29.9 / 37.7 us;
+// 64 queries in 1 / 2: 62 / 85 us. At 8 heads of 64 + 16 dims, where blocks and joins cost less, its choices
+// are the fastest measured too: 45.3 / 14.1 / 13.3 / 16.0, 46.2 / 21.2 / 25.7 and 47.8 / 53.4 us. The pairs are
+// this rule's, not the device's. By these costs no call is split into more than kPlanParts ranges of all its
+// queries (93 queries in two each; more queries are not split), so the limit changes no choice: it is what a
+// workspace has to hold (see cache_workspace).
 struct CachePlan {
   int32_t n_splits, split_blocks;
 };

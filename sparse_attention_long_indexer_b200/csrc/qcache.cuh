@@ -25,9 +25,9 @@ constexpr int kScaleGroup = 128;         // latent dims per scale
 constexpr int kScaleExpMax = 100;        // |exponent| of a scale
 constexpr int kRowThreads = 256;         // 8 warps = 8 rows per CTA and pass
 constexpr int kRowWarps = kRowThreads / 32;
-// Resident CTAs per SM, and the most that are launched. 32768 rows written take 16.1 us (4.5 TB/s of the
-// 6.5 a copy reaches); with 8 launched per SM, of which 6 fit, 18.3, and with the next row's loads ahead of
-// the current row's stores, at 4 per SM, 18.2.
+// Resident CTAs per SM, and the most that are launched. 32768 rows written, from inputs that change, take 15.8 to
+// 16.1 us (4.5 TB/s of the 6.5 a copy reaches); with 8 launched per SM, of which 6 fit, 18.3, and with the next
+// row's loads ahead of the current row's stores, at 4 per SM, 18.2.
 constexpr int kRowCtas = 6;
 
 struct QCacheView {
@@ -89,8 +89,8 @@ __device__ __forceinline__ uint32_t e4m3x4(uint32_t a, uint32_t b, uint64_t inv2
   return r;
 }
 // Two E4M3 codes times a scale (packed twice), as two bf16. Codes convert to fp16 and fp16 to fp32
-// exactly; the product with a power of two, and its bf16 form, are exact too. An SM takes 3.0 clocks for a
-// warp's words of four codes; moving sign, exponent and mantissa into a bf16's places and multiplying
+// exactly; the product with a power of two, and its bf16 form, are exact too. An SM takes 3.3 clocks for a
+// warp's words of four codes (512 threads); moving sign, exponent and mantissa into a bf16's places and multiplying
 // there takes fewer instructions but 4.5 clocks, as most of them are integer ones.
 __device__ __forceinline__ uint32_t expand2(uint16_t codes, uint64_t scale2) {
   uint32_t h;
