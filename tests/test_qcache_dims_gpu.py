@@ -1,8 +1,8 @@
-"""More rows in a call than the cache holds: gathers of many queries' selections, and padded writes."""
+"""More rows in a call than the cache holds (gathers of many queries' selections, padded writes), and very long caches."""
 import pytest
 import torch
 
-from tests.qcache_cases import code_values, dequantised, quantise_latent
+from tests.qcache_cases import attend, check, code_values, dequantised, quantise_latent
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,20 @@ def test_a_padded_write_and_read_of_more_rows_than_the_cache_holds():
     dsa.qcache_write(dims, cache, latent.cuda(), None, ws)
     torch.cuda.synchronize()
     assert dsa.dsa_get_device_status(ws.buf)[0] == dsa.DSA_ERR_INDEX_RANGE
+
+
+def test_the_attention_over_a_cache_longer_than_a_decode_selection():
+    cap, topk = 20_000_000, 130
+    g = torch.Generator().manual_seed(92)
+    dims = dsa.make_dims(1, 1, cap, n_heads=2, d_latent=16, d_rope=8, idx_dim=16)
+    ws = dsa.Workspace.create_qcache(dims, topk)
+    cache = dsa.QCache.create(dims)
+    at = torch.cat([torch.randint(0, cap, (topk - 2,), generator=g), torch.tensor([0, cap - 1])])
+    cache.codes[0, at.cuda()] = torch.randint(0, 120, (topk, 16), generator=g).to(torch.uint8).cuda()
+    cache.scales[0, at.cuda()] = 2.0 ** -6
+    cache.rope[0, at.cuda()] = torch.randn((topk, 8), generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn((1, 1, 2, 24), generator=g).to(torch.bfloat16)
+    out, lse = dsa.sparse_mla_attn_qcache(dims, q.cuda(), cache, at.to(torch.int32).view(1, 1, -1).cuda(), topk, ws)
+    ws.check()
+    rows = dequantised(cache.codes[0, at.cuda()].cpu(), cache.scales[0, at.cuda()].cpu(), cache.rope[0, at.cuda()].cpu())
+    check(out[0, 0], lse[0, 0], attend(q[0, 0].double(), rows, 16, dims.softmax_scale))
